@@ -51,6 +51,7 @@ extern "C" {
 #endif
 
 typedef uint16_t rmm_bf16; /* IEEE bfloat16 bit pattern */
+typedef uint8_t rmm_e4m3;  /* 8-bit floating point, 4 exponent and 3 fraction bits (no infinities, largest 448) */
 typedef void* rmm_stream;  /* cudaStream_t */
 
 typedef enum {
@@ -256,6 +257,65 @@ size_t rmm_linear_int8_workspace_bytes(int64_t n, int64_t d, int64_t m, double r
 rmm_status rmm_linear_int8(const rmm_bf16* A, int64_t n, int64_t d, int64_t lda, const int8_t* Wq, int64_t m,
                            int64_t ldw, const float* scale, rmm_bf16* Y, int64_t ldy, double rho, int32_t* idx_out,
                            void* ws, size_t ws_bytes, rmm_stream stream);
+
+/* ---------------------------------------------------------------- fp8 operands
+ * e4m3 operands with fp32 scales, for the dense products below (rho = 1: no
+ * selection; blocks of kept rows would straddle the scale blocks).
+ *
+ * rmm_quantize_fp8: activations, one scale per row and block of 128 columns,
+ *   a = max |X[i, 128 b : 128 b + 128]|,  sx[b][i] = fl(a / 448), or 1 if that is 0,
+ *   Xq[i, j] = e4m3(fl(X[i, j] / sx[b][i])),
+ * both divisions IEEE fp32, e4m3 to nearest even.  A block that holds a NaN has
+ * a NaN scale; one that holds an infinity has an infinite one.
+ *   X   device bf16 [n][ldx], ldx >= d, a multiple of 8.
+ *   Xq  device e4m3 [n][ldq], ldq >= d, a multiple of 16 (columns past d are not written).
+ *   sx  device fp32 [ceil(d / 128)][lds], lds >= n: a block's scales side by side.
+ * rmm_quantize_fp8_weight: weights, one scale per block of 128 x 128, of `groups`
+ * matrices (w_stride and q_stride elements apart; ignored for one).
+ *   W   device bf16 [groups][d][ldw], Wq device e4m3 [groups][d][ldq].
+ *   sw  device fp32 [groups][ceil(d / 128)][ceil(m / 128)], contiguous.
+ * n = 0 is valid and does nothing.  Limits: d <= 2^24 (activations), fewer than
+ * 2^31 blocks.  No workspace. */
+rmm_status rmm_quantize_fp8(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, rmm_e4m3* Xq, int64_t ldq, float* sx,
+                            int64_t lds, rmm_stream stream);
+rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_stride, int64_t d, int64_t m, int64_t ldw,
+                                   rmm_e4m3* Wq, int64_t q_stride, int64_t ldq, float* sw, rmm_stream stream);
+
+/* rmm_linear_fp8: Y = X W on quantised operands,
+ *   Y[i, c] = sum_b sx[b][i] sw[b][c / 128] sum_{j in block b} Xq[i, j] Wq[j, c],
+ * the inner sums and the outer one in fp32, one rounding to bf16.
+ *   Xq, sx  as rmm_quantize_fp8 writes them (any scales may be used).
+ *   Wq      device e4m3 [d][ldw], ldw >= m, a multiple of 16 (contraction index as the row).
+ *   sw      device fp32 [ceil(d / 128)][ceil(m / 128)].
+ *   Y       device bf16 [n][ldy].
+ * n = 0 is valid and does nothing.  Limits: n, d, m < 2^31 - 512.  No workspace. */
+rmm_status rmm_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
+                          const rmm_e4m3* Wq, int64_t m, int64_t ldw, const float* sw, rmm_bf16* Y, int64_t ldy,
+                          rmm_stream stream);
+
+/* ---------------------------------------------------------------- products grouped by expert
+ * The projections of a mixture-of-experts block: rows sorted by expert, group e
+ * being rows offsets[e] <= i < offsets[e + 1],
+ *   Y[i, :] = X[i, :] . W[e]   (rmm_grouped_linear, bf16; rmm_grouped_linear_fp8,
+ *                               operands and sums as in rmm_linear_fp8)
+ *   X, Xq    device [n][ldx].
+ *   W, Wq    device [groups][d][ldw], w_stride elements between groups (ignored for one).
+ *   sw       device fp32 [groups][ceil(d / 128)][ceil(m / 128)].
+ *   offsets  device int32 [groups + 1], read by the kernel (no synchronisation):
+ *            non-decreasing; a group may be empty.  Values are clamped to
+ *            0 <= ... <= n and to be non-decreasing, so no value reads or writes
+ *            out of range.
+ *   Y        device bf16 [n][ldy]; rows before offsets[0] and from offsets[groups]
+ *            on are left as they were.
+ * The rows a tile takes go by n / groups: uneven groups are right, only slower.
+ * n = 0 is valid and does nothing.  Limits: groups <= 1024; n, d, m < 2^31 - 512.
+ * No workspace. */
+rmm_status rmm_grouped_linear(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, const rmm_bf16* W, int64_t groups,
+                              int64_t w_stride, int64_t m, int64_t ldw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy,
+                              rmm_stream stream);
+rmm_status rmm_grouped_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
+                                  const rmm_e4m3* Wq, int64_t groups, int64_t w_stride, int64_t m, int64_t ldw,
+                                  const float* sw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy, rmm_stream stream);
 
 /* ---------------------------------------------------------------- MLP block
  * The gate / up / down projections of a gated MLP ("Algorithm Deep-Dive: RMM",

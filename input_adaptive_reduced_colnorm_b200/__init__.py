@@ -14,6 +14,7 @@ import ctypes
 import os
 
 __all__ = ["lib", "rmm_k", "select", "linear", "gather_columns", "gather_rows", "gemm_packed", "gemm_gathered", "qk", "pv",
+           "quantize_fp8", "quantize_fp8_weight", "linear_fp8", "grouped_linear", "grouped_linear_fp8",
            "RMMError", "device_error", "library_path"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -71,6 +72,15 @@ _SIGNATURES = {
     "rmm_decode_pv_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_dbl]),
     "rmm_decode_pv": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_dbl,
                                _c_p, _c_p, _c_size, _c_p]),
+    "rmm_quantize_fp8": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+    "rmm_quantize_fp8_weight": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p,
+                                         _c_p]),
+    "rmm_linear_fp8": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+                                _c_p]),
+    "rmm_grouped_linear": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p,
+                                    _c_i64, _c_p]),
+    "rmm_grouped_linear_fp8": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64,
+                                        _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p]),
     "rmm_status_string": (ctypes.c_char_p, [_c_int]),
     "rmm_last_error": (ctypes.c_char_p, []),
     "rmm_device_error": (_c_int, [ctypes.POINTER(ctypes.c_int32)]),
@@ -426,6 +436,183 @@ def decode_pv(P, V, rho: float, *, nk=None, out=None, return_idx: bool = False, 
     _check(Lb.rmm_decode_pv(_ptr(P), _ptr(V), _ptr(out), b, hq, hkv, nk, L, cap, dh, float(rho), _ptr(idx),
                             _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
     return (out, idx) if return_idx else out
+
+
+def _current_device(device):
+    """Makes ``device`` current for the library's launches (a no-op where it is)."""
+    import contextlib
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one device")
+
+
+def _rows(t, name):
+    """Elements between the rows of a matrix (or batch of matrices), whose columns must be next to one another."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} needs unit column stride")
+    return t.stride(-2)
+
+
+def _padded_empty(shape, dtype, device, unit):
+    """An uninitialised tensor whose leading dimension is a multiple of ``unit`` elements."""
+    import torch
+    cols = shape[-1]
+    ld = (cols + unit - 1) // unit * unit
+    t = torch.empty((*shape[:-1], ld), dtype=dtype, device=device)
+    return t if ld == cols else t[..., :cols]
+
+
+def quantize_fp8(X, *, out=None, scale=None):
+    """Activations in e4m3 with one fp32 scale per row and block of 128 columns.
+
+    X [n, d] bf16 CUDA (row stride a multiple of 8) -> (Xq [n, d] float8_e4m3fn, scales [ceil(d / 128), n] float32)
+    with X ~ Xq * scale: scale = max |x| of the block / 448 (1 where that is 0), Xq = x / scale to nearest even.
+    ``out`` needs a row stride that is a multiple of 16 bytes."""
+    import torch
+    _require(X, "X", torch.bfloat16, 2)
+    n, d = X.shape
+    dev = X.device
+    blocks = (d + 127) // 128
+    if out is None:
+        out = _padded_empty((n, d), torch.float8_e4m3fn, dev, 16)
+    if scale is None:
+        scale = torch.empty((blocks, n), dtype=torch.float32, device=dev)
+    _require(out, "out", torch.float8_e4m3fn, 2)
+    _require(scale, "scale", torch.float32, 2)
+    if out.shape != X.shape or scale.shape != (blocks, n):
+        raise ValueError(f"out must be {tuple(X.shape)} and scale {(blocks, n)}")
+    _same_device(X, out, scale)
+    with _current_device(dev):
+        _check(lib().rmm_quantize_fp8(_ptr(X), n, d, _rows(X, "X"), _ptr(out), _rows(out, "out"), _ptr(scale),
+                                      _rows(scale, "scale"), _stream(dev)))
+    return out, scale
+
+
+def quantize_fp8_weight(W, *, out=None, scale=None):
+    """Weights in e4m3 with one fp32 scale per block of 128 x 128.
+
+    W [d, m] or [groups, d, m] bf16 CUDA -> (Wq of W's shape, float8_e4m3fn, scales [(groups,) ceil(d / 128),
+    ceil(m / 128)] float32), as linear_fp8 and grouped_linear_fp8 take them."""
+    import torch
+    _require(W, "W", torch.bfloat16)
+    if W.dim() not in (2, 3):
+        raise ValueError("W must be [d, m] or [groups, d, m]")
+    dev = W.device
+    d, m = W.shape[-2:]
+    shape = (*W.shape[:-2], (d + 127) // 128, (m + 127) // 128)
+    if out is None:
+        out = _padded_empty(tuple(W.shape), torch.float8_e4m3fn, dev, 16)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    _require(out, "out", torch.float8_e4m3fn, W.dim())
+    _require(scale, "scale", torch.float32, W.dim())
+    if out.shape != W.shape or tuple(scale.shape) != shape or not scale.is_contiguous():
+        raise ValueError(f"out must be {tuple(W.shape)} and scale {shape}, contiguous")
+    _same_device(W, out, scale)
+    groups = W.shape[0] if W.dim() == 3 else 1
+    ws, qs = (W.stride(0), out.stride(0)) if W.dim() == 3 else (0, 0)
+    with _current_device(dev):
+        _check(lib().rmm_quantize_fp8_weight(_ptr(W), groups, ws, d, m, _rows(W, "W"), _ptr(out), qs, _rows(out, "out"),
+                                             _ptr(scale), _stream(dev)))
+    return out, scale
+
+
+def _product_out(out, n, m, device):
+    import torch
+    if out is None:
+        return _padded_empty((n, m), torch.bfloat16, device, 8)
+    _require(out, "out", torch.bfloat16, 2)
+    if out.shape != (n, m):
+        raise ValueError(f"out must be {(n, m)}")
+    return out
+
+
+def linear_fp8(Xq, x_scale, Wq, w_scale, *, out=None):
+    """Y = (Xq * x_scale) . (Wq * w_scale) with fp32 sums, for operands as quantize_fp8 and quantize_fp8_weight give
+    them: Xq [n, d] and Wq [d, m] float8_e4m3fn (row strides multiples of 16 bytes), x_scale [ceil(d / 128), n],
+    w_scale [ceil(d / 128), ceil(m / 128)] float32, CUDA.  Returns Y [n, m] bf16."""
+    import torch
+    _require(Xq, "Xq", torch.float8_e4m3fn, 2)
+    _require(Wq, "Wq", torch.float8_e4m3fn, 2)
+    _require(x_scale, "x_scale", torch.float32, 2)
+    _require(w_scale, "w_scale", torch.float32, 2)
+    n, d = Xq.shape
+    d2, m = Wq.shape
+    if d2 != d:
+        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {d2} rows")
+    blocks = (d + 127) // 128
+    if x_scale.shape != (blocks, n) or w_scale.shape != (blocks, (m + 127) // 128) or not w_scale.is_contiguous():
+        raise ValueError(f"x_scale must be {(blocks, n)} and w_scale {(blocks, (m + 127) // 128)}, contiguous")
+    dev = Xq.device
+    out = _product_out(out, n, m, dev)
+    _same_device(Xq, Wq, x_scale, w_scale, out)
+    with _current_device(dev):
+        _check(lib().rmm_linear_fp8(_ptr(Xq), n, d, _rows(Xq, "Xq"), _ptr(x_scale), _rows(x_scale, "x_scale"), _ptr(Wq),
+                                    m, _rows(Wq, "Wq"), _ptr(w_scale), _ptr(out), _rows(out, "out"), _stream(dev)))
+    return out
+
+
+def _check_groups(offsets, groups):
+    import torch
+    _require(offsets, "offsets", torch.int32, 1)
+    if offsets.numel() != groups + 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets must hold {groups + 1} contiguous entries (one more than the groups)")
+
+
+def grouped_linear(X, W, offsets, *, out=None):
+    """Y[i] = X[i] . W[e] for offsets[e] <= i < offsets[e + 1]: the projections of a mixture-of-experts block, rows
+    sorted by expert.  X [n, d], W [groups, d, m] bf16, offsets [groups + 1] int32, CUDA (read by the kernel: the
+    call does not synchronise; values are clamped to 0 <= ... <= n and to be non-decreasing).  Returns Y [n, m]
+    bf16; rows in no group are left as they were (uninitialised without ``out``)."""
+    import torch
+    _require(X, "X", torch.bfloat16, 2)
+    _require(W, "W", torch.bfloat16, 3)
+    n, d = X.shape
+    groups, d2, m = W.shape
+    if d2 != d:
+        raise ValueError(f"contraction mismatch: X has {d} columns, W has {d2} rows")
+    _check_groups(offsets, groups)
+    dev = X.device
+    out = _product_out(out, n, m, dev)
+    _same_device(X, W, offsets, out)
+    with _current_device(dev):
+        _check(lib().rmm_grouped_linear(_ptr(X), n, d, _rows(X, "X"), _ptr(W), groups, W.stride(0), m, _rows(W, "W"),
+                                        _ptr(offsets), _ptr(out), _rows(out, "out"), _stream(dev)))
+    return out
+
+
+def grouped_linear_fp8(Xq, x_scale, Wq, w_scale, offsets, *, out=None):
+    """grouped_linear on e4m3 operands with block scales (see linear_fp8): Xq [n, d], Wq [groups, d, m]
+    float8_e4m3fn, x_scale [ceil(d / 128), n], w_scale [groups, ceil(d / 128), ceil(m / 128)] float32."""
+    import torch
+    _require(Xq, "Xq", torch.float8_e4m3fn, 2)
+    _require(Wq, "Wq", torch.float8_e4m3fn, 3)
+    _require(x_scale, "x_scale", torch.float32, 2)
+    _require(w_scale, "w_scale", torch.float32, 3)
+    n, d = Xq.shape
+    groups, d2, m = Wq.shape
+    if d2 != d:
+        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {d2} rows")
+    blocks = (d + 127) // 128
+    w_shape = (groups, blocks, (m + 127) // 128)
+    if x_scale.shape != (blocks, n) or tuple(w_scale.shape) != w_shape or not w_scale.is_contiguous():
+        raise ValueError(f"x_scale must be {(blocks, n)} and w_scale {w_shape}, contiguous")
+    _check_groups(offsets, groups)
+    dev = Xq.device
+    out = _product_out(out, n, m, dev)
+    _same_device(Xq, Wq, x_scale, w_scale, offsets, out)
+    with _current_device(dev):
+        _check(lib().rmm_grouped_linear_fp8(_ptr(Xq), n, d, _rows(Xq, "Xq"), _ptr(x_scale), _rows(x_scale, "x_scale"),
+                                            _ptr(Wq), groups, Wq.stride(0), m, _rows(Wq, "Wq"), _ptr(w_scale),
+                                            _ptr(offsets), _ptr(out), _rows(out, "out"), _stream(dev)))
+    return out
 
 
 def device_error() -> int:

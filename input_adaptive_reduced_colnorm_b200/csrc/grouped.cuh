@@ -1,0 +1,429 @@
+// Products grouped by expert, in bf16 and in e4m3 with block scales:
+//   Y[i, :] = X[i, :] . W[e]          for offsets[e] <= i < offsets[e + 1]
+// with W[e] d x m (contraction index as the row).  With e4m3 operands
+//   Y[i, c] = sum_b sx[b, i] sw[e, b, c / 128] sum_{j in block b} X[i, j] W[e][j, c],
+// b running over blocks of 128 contraction indices.  A plain product is the case
+// of one group.
+//
+// The operands are swapped, D = W^T X^T: the weights' columns fill the M side of
+// the tensor cores (128 lanes of tensor memory), the rows of X the N side, whose
+// width (16 to 256) follows the rows an expert has.  With the rows on the M side
+// an expert with 4 rows would pay for 128.
+//
+// A stage holds 128 bytes of the contraction (64 bf16 or 128 e4m3 indices) for
+// MT x 128 columns of W (MN-major, 128-byte swizzle) and N rows of X (K-major),
+// brought by TMA; what lies past a matrix's edge reads as zeros.  A tile's rows
+// past its group's end belong to the next group: they are multiplied, not stored.
+//
+// Block scales: each 128-deep block gets an accumulator of its own (of two), and
+// the epilogue threads add it, scaled, into fp32 registers.  A thread holds one
+// column of W (one lane of tensor memory) and half of the tile's rows; the
+// scales of the rows, times the weight block's scale, are the same for all lanes
+// of a warp, so each warp keeps them in shared memory and reads them as
+// broadcasts of four.
+//
+// Group bounds are read on the device (the call does not synchronise): every CTA
+// clamps them to 0 <= ... <= n, non-decreasing, and sums the row tiles of the
+// groups before it starts; a tile number is looked up by bisection.
+//
+// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 4-11
+// epilogue (warps 2 and 3 only take part in the set-up).  CG = 2: two CTAs of a
+// cluster form one M = 256 product (256 columns of W x 256 rows of X), each
+// staging its own 128 columns of W and half of the rows.
+#pragma once
+#include <cuda_bf16.h>
+#include "ptx.cuh"
+
+namespace rmm {
+
+constexpr int kGroupedMaxGroups = 1024;
+constexpr int kGroupedThreads = 384;
+
+struct GroupedParams {
+  const int32_t* offsets;  // [groups + 1] on the device, or null: one group of n rows
+  int groups;
+  int n, m;
+  int num_kb;              // 128-byte blocks of the contraction
+  int m_tiles;             // tiles of CG * MT * 128 columns
+  uint16_t* Y;
+  int64_t ldy;
+  // block scales (e4m3)
+  const float* sx;         // [num_kb][lds]
+  int64_t lds;
+  const float* sw;         // [groups][num_kb][sw_cols]
+  int sw_cols;
+};
+
+template <int N, int MT, int CG>
+struct GroupedCfg {
+  static constexpr int A_BYTES = MT * 128 * 128;
+  static constexpr int X_ROWS = N / CG;
+  static constexpr int X_BYTES = X_ROWS * 128;
+  static constexpr int COLS = MT * N;          // accumulator columns of one tile
+  static constexpr int HC = COLS / 2;          // columns of one epilogue thread
+  static constexpr int TMEM_COLS = 2 * COLS;
+  static constexpr int SCALE_BYTES = 8 * 2 * HC * 4;
+  static constexpr int STAGES_FIT = (232448 - 1024 - 256 - SCALE_BYTES - (2 * kGroupedMaxGroups + 2) * 4) / (A_BYTES + X_BYTES);
+  static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
+  static_assert(STAGES >= 3, "at least three stages");
+  static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory");
+  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier area");
+  static int smem_bytes(int groups) {
+    return 1024 + STAGES * (A_BYTES + X_BYTES) + SCALE_BYTES + 256 + (2 * groups + 2) * 4;
+  }
+};
+
+// Clamped group bounds off[0..groups] and the running count of N-row tiles
+// pre[0..groups], by one warp.
+template <int N>
+__device__ __forceinline__ void grouped_bounds(const GroupedParams& p, int* off, int* pre, int lane) {
+  if (p.offsets == nullptr) {
+    if (lane == 0) {
+      off[0] = 0;
+      off[1] = p.n;
+      pre[0] = 0;
+      pre[1] = (p.n + N - 1) / N;
+    }
+    return;
+  }
+  int top = 0;   // largest bound so far
+  for (int b = 0; b <= p.groups; b += 32) {
+    int v = b + lane <= p.groups ? min(p.offsets[b + lane], p.n) : 0;
+    v = max(v, top);
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, v, s);
+      if (lane >= s) v = max(v, u);
+    }
+    if (b + lane <= p.groups) off[b + lane] = v;
+    top = __shfl_sync(0xffffffffu, v, 31);
+  }
+  __syncwarp();
+  int sum = 0;
+  for (int b = 0; b < p.groups; b += 32) {
+    int v = b + lane < p.groups ? (off[b + lane + 1] - off[b + lane] + N - 1) / N : 0;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, v, s);
+      if (lane >= s) v += u;
+    }
+    if (b + lane < p.groups) pre[b + lane + 1] = sum + v;
+    sum += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) pre[0] = 0;
+}
+
+struct GroupedTile {
+  int group, row0, row_end, mtile;
+};
+
+// Tile order: group, then column tile, then row tile fastest, so that the row
+// tiles of one piece of the weights run side by side and share it through L2.
+template <int N>
+__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, const int* off, const int* pre, int tile) {
+  int lo = 0, hi = p.groups - 1;  // the last group whose first tile is <= tile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] * p.m_tiles <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  const int rt = pre[lo + 1] - pre[lo];
+  const int r = tile - pre[lo] * p.m_tiles;
+  GroupedTile t;
+  t.group = lo;
+  t.mtile = r / rt;
+  t.row0 = off[lo] + (r - t.mtile * rt) * N;
+  t.row_end = off[lo + 1];
+  return t;
+}
+
+__device__ __forceinline__ uint64_t grouped_fma2(uint64_t a, uint64_t b, uint64_t c) {  // a * b + c, two fp32
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+template <bool FP8, int N, int MT, int CG>
+__global__ void __launch_bounds__(kGroupedThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const GroupedParams p) {
+  using C = GroupedCfg<N, MT, CG>;
+  constexpr int STAGES = C::STAGES, HC = C::HC;
+  constexpr int BK = FP8 ? 128 : 64;
+  constexpr uint32_t IDESC = FP8 ? make_idesc_e4m3(128 * CG, N, 1, 0) : make_idesc_bf16(128 * CG, N, 1, 0);
+  // bytes between the k-steps of W in a stage (16 bf16 or 32 e4m3 rows of 128 bytes)
+  constexpr uint32_t A_STEP = FP8 ? 4096 : 2048;
+
+  extern __shared__ uint8_t grouped_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(grouped_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sX = smem + STAGES * C::A_BYTES;
+  float* sScale = reinterpret_cast<float*>(sX + STAGES * C::X_BYTES);  // [8 warps][2][HC]
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sScale) + C::SCALE_BYTES);  // even CTA
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;  // even CTA
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
+  int* pre = off + p.groups + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;  // 0: the CTA that issues the MMAs
+  const int worker = static_cast<int>(blockIdx.x) / CG, workers = static_cast<int>(gridDim.x) / CG;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 8 * CG);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+  }
+  if (warp == 1) {
+    if (CG == 2) {
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  wait_prior_kernels();  // bounds, operands and the output are touched only after this
+  if (warp == 2) grouped_bounds<N>(p, off, pre, lane);
+  tc_fence_before();
+  if (CG == 2) cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = pre[p.groups] * p.m_tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      const uint32_t full_even = CG == 2 ? map_shared_rank(smem_u32(&full[0]), 0u) : 0u;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (int tile = worker; ok && tile < total; tile += workers) {
+        const GroupedTile t = grouped_tile<N>(p, off, pre, tile);
+        const int f0 = (t.mtile * CG + static_cast<int>(rank)) * MT * 128;
+        const int row = t.row0 + static_cast<int>(rank) * C::X_ROWS;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * (C::A_BYTES + C::X_BYTES));
+          uint8_t* a = sA + stage * C::A_BYTES;
+          uint8_t* x = sX + stage * C::X_BYTES;
+          constexpr int BOXES = FP8 ? MT : 2 * MT;     // boxes of 128 bytes of columns
+          constexpr int BOX_COLS = FP8 ? 128 : 64;
+          if (CG == 2) {
+            const uint32_t bar = full_even + 8u * static_cast<uint32_t>(stage);
+#pragma unroll
+            for (int j = 0; j < BOXES; ++j)
+              tma_load_3d_pair(a + j * (BK * 128), &tmW, bar, f0 + j * BOX_COLS, kb * BK, t.group);
+            tma_load_2d_pair(x, &tmX, bar, kb * BK, row);
+          } else {
+#pragma unroll
+            for (int j = 0; j < BOXES; ++j)
+              tma_load_3d(a + j * (BK * 128), &tmW, &full[stage], f0 + j * BOX_COLS, kb * BK, t.group);
+            tma_load_2d(x, &tmX, &full[stage], kb * BK, row);
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // wait (bounded) for the stages filled so far, so no copy lands after exit
+        for (int s = 0; s < STAGES; ++s) {
+          const uint32_t uses = (issued + STAGES - 1 - s) / STAGES;
+          if (uses == 0) continue;
+          const uint32_t a = smem_u32(&full[s]);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(a, (uses - 1) & 1u) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0 && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t acc_i = 0;
+      bool ok = true;
+      for (int tile = worker; ok && tile < total; tile += workers) {
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          const uint32_t acc = acc_i & 1u;
+          if (FP8 || kb == 0) {
+            if (!mbar_wait(&tempty[acc], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, CG == 2)) {
+              ok = false;
+              break;
+            }
+          }
+          if (!mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * C::COLS;
+          const uint32_t a0 = smem_u32(sA + stage * C::A_BYTES);
+          const uint32_t x0 = smem_u32(sX + stage * C::X_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t xd = make_sw128_desc(x0 + kk * 32, 16, 1024);
+            const uint32_t add = (kk != 0 || (!FP8 && kb != 0)) ? 1u : 0u;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint64_t ad = make_sw128_desc(a0 + mt * 16384 + kk * A_STEP, 8192, 1024);
+              const uint32_t d = d_tmem + static_cast<uint32_t>(mt * N);
+              if (CG == 2) {
+                if (FP8) umma_e4m3_pair(d, ad, xd, IDESC, add);
+                else umma_bf16_pair(d, ad, xd, IDESC, add);
+              } else {
+                if (FP8) umma_e4m3(d, ad, xd, IDESC, add);
+                else umma_bf16(d, ad, xd, IDESC, add);
+              }
+            }
+          }
+          if (CG == 2) umma_commit_pair(&empty[stage], 0x3);
+          else umma_commit(&empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (FP8 || kb == p.num_kb - 1) {
+            if (CG == 2) umma_commit_pair(&tfull[acc], 0x3);
+            else umma_commit(&tfull[acc]);
+            ++acc_i;
+          }
+        }
+      }
+      // every MMA issued by this thread is complete once `drain` flips
+      if (CG == 2) umma_commit_pair(drain, 0x1);
+      else umma_commit(drain);
+      const uint32_t a = smem_u32(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int half = (warp - 4) >> 2;
+    // this thread's accumulator columns [half * HC, half * HC + HC): rows of X
+    // row_of(i), columns of W in 128-column tile mt_of(i)
+    const int mt0 = HC >= N ? half * (HC / N) : 0;
+    const int r0 = HC >= N ? 0 : half * HC;
+    auto mt_of = [&](int i) { return HC >= N ? mt0 + i / N : 0; };
+    auto row_of = [&](int i) { return HC >= N ? i % N : r0 + i; };
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HC);
+    const uint32_t tempty_even = CG == 2 ? map_shared_rank(smem_u32(&tempty[0]), 0u) : 0u;
+    float* my_scale = sScale + (warp - 4) * 2 * HC;
+    uint32_t acc_i = 0;
+    bool ok = true;
+    auto release = [&](uint32_t acc) {  // this warp has read the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_cluster(tempty_even + 8u * acc);
+      }
+    };
+    for (int tile = worker; ok && tile < total; tile += workers) {
+      const GroupedTile t = grouped_tile<N>(p, off, pre, tile);
+      const int mblock0 = (t.mtile * CG + static_cast<int>(rank)) * MT;  // first 128-column tile
+      auto store = [&](int i, float v) {
+        const int row = t.row0 + row_of(i);
+        const int f = (mblock0 + mt_of(i)) * 128 + quarter * 32 + lane;
+        if (row < t.row_end && f < p.m)
+          reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<int64_t>(row) * p.ldy + f] = __float2bfloat16_rn(v);
+      };
+      if (FP8) {
+        uint64_t sum[HC / 2];
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) sum[i] = 0;
+        for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
+          const uint32_t acc = acc_i & 1u;
+          float* sc = my_scale + acc * HC;
+#pragma unroll
+          for (int i = 0; i < HC / 32; ++i) {
+            const int c = i * 32 + lane;
+            const int row = t.row0 + row_of(c);
+            const int mb = mblock0 + mt_of(c);
+            float v = 0.f;
+            if (row < t.row_end && mb < p.sw_cols)
+              v = __ldg(p.sx + kb * p.lds + row) *
+                  __ldg(p.sw + (static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb);
+            sc[c] = v;
+          }
+          __syncwarp();
+          if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < HC / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(lane_base + acc * C::COLS + c * 32, r);
+            tmem_ld_wait();
+            if (c == HC / 32 - 1) release(acc);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(sc + c * 32 + e);
+              uint64_t& a = sum[(c * 32 + e) / 2];
+              uint64_t& b = sum[(c * 32 + e) / 2 + 1];
+              a = grouped_fma2(static_cast<uint64_t>(r[e]) | (static_cast<uint64_t>(r[e + 1]) << 32), s2.x, a);
+              b = grouped_fma2(static_cast<uint64_t>(r[e + 2]) | (static_cast<uint64_t>(r[e + 3]) << 32), s2.y, b);
+            }
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) {
+          store(2 * i, __uint_as_float(static_cast<uint32_t>(sum[i])));
+          store(2 * i + 1, __uint_as_float(static_cast<uint32_t>(sum[i] >> 32)));
+        }
+      } else {
+        const uint32_t acc = acc_i & 1u;
+        if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue, 64)) break;
+        tc_fence_after();
+        for (int c = 0; c < HC / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(lane_base + acc * C::COLS + c * 32, r);
+          tmem_ld_wait();
+          if (c == HC / 32 - 1) release(acc);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) store(c * 32 + e, __uint_as_float(r[e]));
+        }
+        ++acc_i;
+      }
+    }
+  }
+
+  tc_fence_before();
+  if (CG == 2) cluster_sync();  // both CTAs are done with every MMA, copy and accumulator
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if (CG == 2) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace rmm

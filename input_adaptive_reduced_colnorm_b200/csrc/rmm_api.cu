@@ -23,6 +23,8 @@
 #include "gemv_i8.cuh"
 #include "attention.cuh"
 #include "decode_select.cuh"
+#include "quantize.cuh"
+#include "grouped.cuh"
 
 using namespace rmm;
 
@@ -1894,6 +1896,257 @@ rmm_status rmm_pv(const rmm_bf16* P, const rmm_bf16* V, rmm_bf16* O, int64_t bat
                   : launch_gemm<128, kBTileMN, kEpiBf16, kCausalNone>(ta, tb, g, s);
   return causal ? launch_gemm<64, kBTileMN, kEpiBf16, kCausalLimitK>(ta, tb, g, s)
                 : launch_gemm<64, kBTileMN, kEpiBf16, kCausalNone>(ta, tb, g, s);
+}
+
+// ---------------------------------------------------------------- fp8 and grouped products
+}  // extern "C"
+
+namespace {
+
+// X [n][ldx] and W [groups][d][ldw] (w_stride elements between groups) as boxes
+// of 128 bytes x rows, elements past an edge read as zero.
+rmm_status make_tmaps_grouped(CUtensorMap* tw, CUtensorMap* tx, bool fp8, const void* W, int64_t groups, int64_t d,
+                              int64_t m, int64_t ldw, int64_t w_stride, const void* X, int64_t n, int64_t ldx,
+                              int x_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return fail(RMM_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t eb = fp8 ? 1 : 2;
+  const cuuint32_t bk = fp8 ? 128 : 64;
+  cuuint32_t estr[3] = {1, 1, 1};
+  cuuint64_t wd[3] = {static_cast<cuuint64_t>(m), static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(groups)};
+  cuuint64_t ws[2] = {static_cast<cuuint64_t>(ldw) * eb,
+                      static_cast<cuuint64_t>(groups > 1 ? w_stride : d * ldw) * eb};
+  cuuint32_t wb[3] = {bk, bk, 1};
+  CUresult r = fn(tw, type, 3, const_cast<void*>(W), wd, ws, wb, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(RMM_ERR_CUDA, "cuTensorMapEncodeTiled (weights) failed (%d)", static_cast<int>(r));
+  cuuint64_t xd[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n)};
+  cuuint64_t xs[1] = {static_cast<cuuint64_t>(ldx) * eb};
+  cuuint32_t xb[2] = {bk, static_cast<cuuint32_t>(x_rows)};
+  r = fn(tx, type, 2, const_cast<void*>(X), xd, xs, xb, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(RMM_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", static_cast<int>(r));
+  return RMM_OK;
+}
+
+struct GroupedCall {
+  bool fp8;
+  const void* X;
+  int64_t n, d, ldx;
+  const void* W;
+  int64_t groups, w_stride, m, ldw;
+  GroupedParams p;
+};
+
+template <bool FP8, int N, int MT, int CG>
+rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
+  using Cfg = GroupedCfg<N, MT, CG>;
+  CUtensorMap tw, tx;
+  if (rmm_status st = make_tmaps_grouped(&tw, &tx, FP8, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx,
+                                         Cfg::X_ROWS))
+    return st;
+  GroupedParams p = c.p;
+  p.num_kb = static_cast<int>(ceil_div(c.d, FP8 ? 128 : 64));
+  p.m_tiles = static_cast<int>(ceil_div(c.m, CG * MT * 128));
+  // row tiles: at most n / N whole ones and a partial one per group
+  const int64_t row_tiles = ceil_div(c.n, N) + std::min<int64_t>(c.groups - 1, c.n);
+  if (row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
+  const int64_t workers = std::min<int64_t>(row_tiles * p.m_tiles, std::max(1, num_sms() / CG));
+  const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
+  auto kern = grouped_kernel<FP8, N, MT, CG>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
+  const dim3 grid(static_cast<unsigned>(workers * CG));
+  if (CG == 2) e = launch_cluster(kern, grid, dim3(kGroupedThreads), smem, 2, s, tw, tx, p);
+  else e = launch_chained(kern, grid, dim3(kGroupedThreads), smem, s, tw, tx, p);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
+  return RMM_OK;
+}
+
+template <bool FP8>
+rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
+  const int64_t rows = ceil_div(c.n, c.groups);  // of an average group
+  if (rows <= 16) return launch_grouped_t<FP8, 16, 4, 1>(c, s);
+  if (rows <= 32) return launch_grouped_t<FP8, 32, 4, 1>(c, s);
+  if (rows <= 64) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
+  if (rows <= 128) return launch_grouped_t<FP8, 128, 2, 1>(c, s);
+  return launch_grouped_t<FP8, 256, 1, 2>(c, s);
+}
+
+// Checks shared by the product calls; `unit` = elements of 16 bytes.
+rmm_status check_product(const void* X, int64_t n, int64_t d, int64_t ldx, const void* W, int64_t groups,
+                         int64_t w_stride, int64_t m, int64_t ldw, const void* Y, int64_t ldy, int64_t unit) {
+  if (n < 0 || d < 1 || m < 1 || groups < 1)
+    return fail(RMM_ERR_INVALID_ARG, "n must be >= 0; d, m and groups must be >= 1");
+  if (W == nullptr || (n > 0 && (X == nullptr || Y == nullptr))) return fail(RMM_ERR_INVALID_ARG, "X, W and Y are required");
+  if (ldx < d || ldw < m || ldy < m) return fail(RMM_ERR_INVALID_ARG, "leading dimension too small");
+  if (n > kIntMax - 256 || d > kIntMax - 256 || m > kIntMax - 512 || ldx > (1LL << 36) || ldw > (1LL << 36) ||
+      ldy > (1LL << 36) || d * ldw > (1LL << 38))
+    return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
+  if (groups > kGroupedMaxGroups) return fail(RMM_ERR_UNSUPPORTED, "at most %d groups", kGroupedMaxGroups);
+  if (groups > 1 && w_stride < (d - 1) * ldw + m) return fail(RMM_ERR_INVALID_ARG, "the groups' weights overlap");
+  if (groups > 1 && w_stride > (1LL << 38)) return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
+  if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || ldx % unit || ldw % unit || ldy % 8 ||
+      (groups > 1 && w_stride % unit))
+    return fail(RMM_ERR_UNSUPPORTED, "pointers 16-byte aligned; ldx, ldw and the group stride multiples of %d, ldy of 8",
+                static_cast<int>(unit));
+  return RMM_OK;
+}
+
+rmm_status check_scales(const float* sx, int64_t lds, int64_t n, const float* sw) {
+  if (sw == nullptr || (n > 0 && sx == nullptr)) return fail(RMM_ERR_INVALID_ARG, "the scales are required");
+  if (lds < n) return fail(RMM_ERR_INVALID_ARG, "lds must be >= n");
+  if ((reinterpret_cast<uintptr_t>(sx) & 3u) || (reinterpret_cast<uintptr_t>(sw) & 3u))
+    return fail(RMM_ERR_UNSUPPORTED, "scales must be 4-byte aligned");
+  return RMM_OK;
+}
+
+rmm_status fp8_product(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
+                       const rmm_e4m3* Wq, int64_t groups, int64_t w_stride, int64_t m, int64_t ldw, const float* sw,
+                       const int32_t* offsets, rmm_bf16* Y, int64_t ldy, cudaStream_t s) {
+  if (rmm_status st = check_product(Xq, n, d, ldx, Wq, groups, w_stride, m, ldw, Y, ldy, 16)) return st;
+  if (rmm_status st = check_scales(sx, lds, n, sw)) return st;
+  if (n == 0) return RMM_OK;
+  GroupedCall c{};
+  c.X = Xq;
+  c.n = n;
+  c.d = d;
+  c.ldx = ldx;
+  c.W = Wq;
+  c.groups = groups;
+  c.w_stride = w_stride;
+  c.m = m;
+  c.ldw = ldw;
+  c.p.offsets = offsets;
+  c.p.groups = static_cast<int>(groups);
+  c.p.n = static_cast<int>(n);
+  c.p.m = static_cast<int>(m);
+  c.p.Y = Y;
+  c.p.ldy = ldy;
+  c.p.sx = sx;
+  c.p.lds = lds;
+  c.p.sw = sw;
+  c.p.sw_cols = static_cast<int>(ceil_div(m, 128));
+  return launch_grouped<true>(c, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+rmm_status rmm_quantize_fp8(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, rmm_e4m3* Xq, int64_t ldq, float* sx,
+                            int64_t lds, rmm_stream stream) {
+  t_last_error.clear();
+  if (n < 0 || d < 1) return fail(RMM_ERR_INVALID_ARG, "n must be >= 0 and d >= 1");
+  if (n > 0 && (X == nullptr || Xq == nullptr || sx == nullptr)) return fail(RMM_ERR_INVALID_ARG, "X, Xq and sx are required");
+  if (ldx < d || ldq < d || lds < n) return fail(RMM_ERR_INVALID_ARG, "leading dimension too small");
+  if (!aligned16(X) || !aligned16(Xq) || (reinterpret_cast<uintptr_t>(sx) & 3u) || ldx % 8 || ldq % 16)
+    return fail(RMM_ERR_UNSUPPORTED, "X and Xq 16-byte aligned; ldx a multiple of 8, ldq of 16");
+  if (n > kIntMax - 256 || d > (1LL << 24) || ldx > (1LL << 36) || ldq > (1LL << 36))
+    return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
+  if (n == 0) return RMM_OK;
+  QuantParams p{};
+  p.x = X;
+  p.ldx = ldx;
+  p.q = Xq;
+  p.ldq = ldq;
+  p.s = sx;
+  p.lds = lds;
+  p.n = n;
+  p.d = d;
+  const int64_t blocks = ceil_div(d, 128);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (n < 16)
+    e = launch_chained(quantize_rows_kernel<1, 1>, dim3(static_cast<unsigned>(n), static_cast<unsigned>(ceil_div(blocks, 16))),
+                       dim3(256), 0, s, p);
+  else
+    e = launch_chained(quantize_rows_kernel<16, 4>,
+                       dim3(static_cast<unsigned>(ceil_div(n, 16)), static_cast<unsigned>(ceil_div(blocks, 4))), dim3(256), 0,
+                       s, p);
+  if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
+  return RMM_OK;
+}
+
+rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_stride, int64_t d, int64_t m, int64_t ldw,
+                                   rmm_e4m3* Wq, int64_t q_stride, int64_t ldq, float* sw, rmm_stream stream) {
+  t_last_error.clear();
+  if (groups < 1 || d < 1 || m < 1) return fail(RMM_ERR_INVALID_ARG, "groups, d and m must be >= 1");
+  if (W == nullptr || Wq == nullptr || sw == nullptr) return fail(RMM_ERR_INVALID_ARG, "W, Wq and sw are required");
+  if (ldw < m || ldq < m) return fail(RMM_ERR_INVALID_ARG, "leading dimension too small");
+  if (d > kIntMax - 256 || m > kIntMax - 256 || ldw > (1LL << 36) || ldq > (1LL << 36) || d * ldw > (1LL << 38) ||
+      d * ldq > (1LL << 38))
+    return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
+  if (groups > 1 && (w_stride < (d - 1) * ldw + m || q_stride < (d - 1) * ldq + m))
+    return fail(RMM_ERR_INVALID_ARG, "the groups' matrices overlap");
+  if (!aligned16(W) || !aligned16(Wq) || (reinterpret_cast<uintptr_t>(sw) & 3u) || ldw % 8 || ldq % 16 ||
+      (groups > 1 && (w_stride % 8 || q_stride % 16)))
+    return fail(RMM_ERR_UNSUPPORTED,
+                "W and Wq 16-byte aligned; ldw and the stride of W multiples of 8, ldq and the stride of Wq of 16");
+  const int64_t db = ceil_div(d, 128), mb = ceil_div(m, 128);
+  if (groups > kIntMax || groups * db > kIntMax || groups * db * mb > kIntMax)
+    return fail(RMM_ERR_UNSUPPORTED, "too many blocks");
+  QuantParams p{};
+  p.x = W;
+  p.ldx = ldw;
+  p.q = Wq;
+  p.ldq = ldq;
+  p.s = sw;
+  p.n = d;
+  p.d = m;
+  p.xstride = w_stride;
+  p.qstride = q_stride;
+  p.dblocks = static_cast<int>(db);
+  p.mblocks = static_cast<int>(mb);
+  const cudaError_t e = launch_chained(quantize_blocks_kernel, dim3(static_cast<unsigned>(groups * db * mb)), dim3(256), 0,
+                                       static_cast<cudaStream_t>(stream), p);
+  if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
+  return RMM_OK;
+}
+
+rmm_status rmm_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
+                          const rmm_e4m3* Wq, int64_t m, int64_t ldw, const float* sw, rmm_bf16* Y, int64_t ldy,
+                          rmm_stream stream) {
+  t_last_error.clear();
+  return fp8_product(Xq, n, d, ldx, sx, lds, Wq, 1, 0, m, ldw, sw, nullptr, Y, ldy, static_cast<cudaStream_t>(stream));
+}
+
+rmm_status rmm_grouped_linear(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, const rmm_bf16* W, int64_t groups,
+                              int64_t w_stride, int64_t m, int64_t ldw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy,
+                              rmm_stream stream) {
+  t_last_error.clear();
+  if (rmm_status st = check_product(X, n, d, ldx, W, groups, w_stride, m, ldw, Y, ldy, 8)) return st;
+  if (offsets == nullptr) return fail(RMM_ERR_INVALID_ARG, "offsets are required");
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
+  if (n == 0) return RMM_OK;
+  GroupedCall c{};
+  c.X = X;
+  c.n = n;
+  c.d = d;
+  c.ldx = ldx;
+  c.W = W;
+  c.groups = groups;
+  c.w_stride = w_stride;
+  c.m = m;
+  c.ldw = ldw;
+  c.p.offsets = offsets;
+  c.p.groups = static_cast<int>(groups);
+  c.p.n = static_cast<int>(n);
+  c.p.m = static_cast<int>(m);
+  c.p.Y = Y;
+  c.p.ldy = ldy;
+  return launch_grouped<false>(c, static_cast<cudaStream_t>(stream));
+}
+
+rmm_status rmm_grouped_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
+                                  const rmm_e4m3* Wq, int64_t groups, int64_t w_stride, int64_t m, int64_t ldw,
+                                  const float* sw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy, rmm_stream stream) {
+  t_last_error.clear();
+  if (offsets == nullptr) return fail(RMM_ERR_INVALID_ARG, "offsets are required");
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
+  return fp8_product(Xq, n, d, ldx, sx, lds, Wq, groups, w_stride, m, ldw, sw, offsets, Y, ldy,
+                     static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

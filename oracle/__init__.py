@@ -494,3 +494,86 @@ def rmm_attention_rows(Qh, Kg, Vg, rho: float, rows=None, causal: bool = True, s
         I = topk_ascending(column_norms(Qh), retention_count(rho, Qh.shape[1]))
     I = _check_index_set(I, Qh.shape[1], "attention")
     return attention_rows(Qh, Kg, Vg, I, rows, causal, scale), I
+
+
+# ------------------------------------------------------------------ fp8 operands and grouped products
+E4M3_MAX = 448.0
+FP8_BLOCK = 128
+
+
+def e4m3_round(x: np.ndarray) -> np.ndarray:
+    """Nearest e4m3 value (4 exponent bits of bias 7, 3 fraction bits, subnormals of
+    step 2^-9, largest 448), ties to even, larger sizes to 448; NaN stays NaN."""
+    x = np.asarray(x, dtype=np.float64)
+    _, e = np.frexp(np.where(np.isfinite(x), x, 1.0))  # |x| in [2^(e-1), 2^e)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.clip(np.rint(x / step) * step, -E4M3_MAX, E4M3_MAX)
+
+
+def _fp8_scale(amax: np.ndarray) -> np.ndarray:
+    with np.errstate(invalid="ignore", over="ignore", under="ignore"):
+        s = np.asarray(amax, dtype=np.float32) / np.float32(E4M3_MAX)
+    return np.where(s == 0, np.float32(1.0), s)
+
+
+def _fp8_codes(x: np.ndarray, s: np.ndarray) -> np.ndarray:
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore", under="ignore"):
+        return e4m3_round(np.asarray(x, dtype=np.float32) / s)
+
+
+def quantize_fp8(X: np.ndarray):
+    """One scale per row and block of 128 columns: s = fl32(max |x| / 448) (1 where
+    that is 0), q = e4m3(fl32(x / s)).  X [n, d] (bf16 values) -> the e4m3 values
+    [n, d] and the fp32 scales [ceil(d / 128), n]."""
+    X = np.asarray(X, dtype=np.float64)
+    n, d = X.shape
+    nb = -(-d // FP8_BLOCK)
+    q = np.empty((n, d))
+    s = np.empty((nb, n), dtype=np.float32)
+    for b in range(nb):
+        cols = slice(b * FP8_BLOCK, min(d, (b + 1) * FP8_BLOCK))
+        s[b] = _fp8_scale(np.abs(X[:, cols]).max(axis=1))
+        q[:, cols] = _fp8_codes(X[:, cols], s[b][:, None])
+    return q, s
+
+
+def quantize_fp8_weight(W: np.ndarray):
+    """One scale per block of 128 x 128.  W [d, m] -> e4m3 values [d, m] and scales
+    [ceil(d / 128), ceil(m / 128)]."""
+    W = np.asarray(W, dtype=np.float64)
+    d, m = W.shape
+    db, mb = -(-d // FP8_BLOCK), -(-m // FP8_BLOCK)
+    q = np.empty((d, m))
+    s = np.empty((db, mb), dtype=np.float32)
+    for b in range(db):
+        for c in range(mb):
+            at = np.s_[b * FP8_BLOCK:(b + 1) * FP8_BLOCK, c * FP8_BLOCK:(c + 1) * FP8_BLOCK]
+            s[b, c] = _fp8_scale(np.abs(W[at]).max())
+            q[at] = _fp8_codes(W[at], s[b, c])
+    return q, s
+
+
+def fp8_widen(q: np.ndarray, s_rows: np.ndarray) -> np.ndarray:
+    """The activations that e4m3 values [n, d] and scales [ceil(d / 128), n] stand for."""
+    q = np.asarray(q, dtype=np.float64)
+    return q * np.repeat(np.asarray(s_rows, dtype=np.float64).T, FP8_BLOCK, axis=1)[:, : q.shape[1]]
+
+
+def fp8_widen_weight(q: np.ndarray, s: np.ndarray) -> np.ndarray:
+    """The weights that e4m3 values [d, m] and 128 x 128 block scales stand for."""
+    q = np.asarray(q, dtype=np.float64)
+    wide = np.repeat(np.repeat(np.asarray(s, dtype=np.float64), FP8_BLOCK, axis=0), FP8_BLOCK, axis=1)
+    return q * wide[: q.shape[0], : q.shape[1]]
+
+
+def grouped_product(X: np.ndarray, W, offsets, Y: np.ndarray) -> np.ndarray:
+    """Y with rows offsets[e] .. offsets[e + 1] - 1 replaced by those of X . W[e]; the
+    bounds clamped to [0, n] and to be non-decreasing, other rows of Y unchanged."""
+    X = np.asarray(X, dtype=np.float64)
+    Y = np.array(Y, dtype=np.float64)
+    bounds = np.maximum.accumulate(np.clip(np.asarray(offsets, dtype=np.int64), 0, X.shape[0]))
+    for e in range(len(bounds) - 1):
+        lo, hi = int(bounds[e]), int(bounds[e + 1])
+        if hi > lo:
+            Y[lo:hi] = X[lo:hi] @ np.asarray(W[e], dtype=np.float64)
+    return Y
