@@ -454,10 +454,11 @@ def _same_device(first, *others):
 
 
 def _rows(t, name):
-    """Elements between the rows of a matrix (or batch of matrices), whose columns must be next to one another."""
+    """Elements between the rows of a matrix (or batch of matrices), whose columns must be next to one another; for
+    one row, whose stride says nothing, a distance that holds it."""
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} needs unit column stride")
-    return t.stride(-2)
+    return t.stride(-2) if t.shape[-2] > 1 else (t.shape[-1] + 15) // 16 * 16
 
 
 def _padded_empty(shape, dtype, device, unit):

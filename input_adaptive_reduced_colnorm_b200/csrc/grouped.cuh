@@ -16,20 +16,26 @@
 // past its group's end belong to the next group: they are multiplied, not stored.
 //
 // Block scales: each 128-deep block gets an accumulator of its own (of two), and
-// the epilogue threads add it, scaled, into fp32 registers.  A thread holds one
-// column of W (one lane of tensor memory) and half of the tile's rows; the
-// scales of the rows, times the weight block's scale, are the same for all lanes
-// of a warp, so each warp keeps them in shared memory and reads them as
-// broadcasts of four.
+// the epilogue threads add it, scaled, into fp32 registers.  They read tensor
+// memory in the 16 x 256-bit shape: a thread gets 2 neighbouring rows of X for 4
+// columns of W out of each 8 x 32, so one pair of row scales (times the weight
+// block's, kept by each warp in shared memory) serves 4 packed multiply-adds.
+// (With a lane's whole row per thread, every multiply-add needed scales of its
+// own: 1 MB of shared-memory reads per 256 x 256 block and SM pair, twice the
+// time of the block's tensor work; 380 TFLOP/s at 4096 x 4096 x 14336.)
+//
+// Tiles are cut to the rows that are there: the N of a tile's instructions is
+// its row count rounded up to 16 (32 for a pair).  When the tiles do not fill a
+// whole number of waves, those of the last wave are cut into narrower ones.
 //
 // Group bounds are read on the device (the call does not synchronise): every CTA
 // clamps them to 0 <= ... <= n, non-decreasing, and sums the row tiles of the
 // groups before it starts; a tile number is looked up by bisection.
 //
-// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 4-11
-// epilogue (warps 2 and 3 only take part in the set-up).  CG = 2: two CTAs of a
-// cluster form one M = 256 product (256 columns of W x 256 rows of X), each
-// staging its own 128 columns of W and half of the rows.
+// Roles (320 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
+// epilogue.  CG = 2: two CTAs of a cluster form one M = 256 product (256 columns
+// of W x 256 rows of X), each staging its own 128 columns of W and half of the
+// rows.
 #pragma once
 #include <cuda_bf16.h>
 #include "ptx.cuh"
@@ -37,7 +43,7 @@
 namespace rmm {
 
 constexpr int kGroupedMaxGroups = 1024;
-constexpr int kGroupedThreads = 384;
+constexpr int kGroupedThreads = 320;
 
 struct GroupedParams {
   const int32_t* offsets;  // [groups + 1] on the device, or null: one group of n rows
@@ -113,34 +119,123 @@ __device__ __forceinline__ void grouped_bounds(const GroupedParams& p, int* off,
   if (lane == 0) pre[0] = 0;
 }
 
+// One piece of work: rows [row0, row_end) (at most w of them) of group `group`
+// times column tile mtile of its weights.
 struct GroupedTile {
-  int group, row0, row_end, mtile;
+  int group, row0, row_end, mtile, w;
 };
 
-// Tile order: group, then column tile, then row tile fastest, so that the row
-// tiles of one piece of the weights run side by side and share it through L2.
-template <int N>
-__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams& p, const int* off, const int* pre, int tile) {
-  int lo = 0, hi = p.groups - 1;  // the last group whose first tile is <= tile
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] * p.m_tiles <= tile) lo = mid;
-    else hi = mid - 1;
+// The tiles of a call as units of work.  Tile order: group, then column tile,
+// then row tile fastest, so that the row tiles of one piece of the weights run
+// side by side and share it through L2.  The tiles past the last whole wave are
+// cut into `cut` pieces of N / cut rows where that lets more workers take part.
+template <int N, int CG>
+struct GroupedUnits {
+  const int *off, *pre;
+  int groups, m_tiles, whole, cut, count;
+  __device__ __forceinline__ GroupedUnits(const GroupedParams& p, const int* off_, const int* pre_, int workers)
+      : off(off_), pre(pre_), groups(p.groups), m_tiles(p.m_tiles), cut(1) {
+    const int tiles = pre[groups] * m_tiles;
+    const int rest = tiles % workers;
+    if (N >= 128 && rest > 0)
+      while (N / cut > 32 * CG && 2 * cut * rest <= workers) cut *= 2;
+    whole = tiles - rest;
+    count = whole + rest * cut;
   }
-  const int rt = pre[lo + 1] - pre[lo];
-  const int r = tile - pre[lo] * p.m_tiles;
-  GroupedTile t;
-  t.group = lo;
-  t.mtile = r / rt;
-  t.row0 = off[lo] + (r - t.mtile * rt) * N;
-  t.row_end = off[lo + 1];
-  return t;
-}
+  __device__ __forceinline__ GroupedTile get(int unit) const {
+    int tile = unit, part = 0;
+    if (N >= 128 && unit >= whole) {
+      tile = whole + (unit - whole) / cut;
+      part = (unit - whole) % cut;
+    }
+    const int width = (N >= 128 && unit >= whole) ? N / cut : N;
+    int lo = 0, hi = groups - 1;  // the last group whose first tile is <= tile
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] * m_tiles <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    const int rt = pre[lo + 1] - pre[lo];
+    const int r = tile - pre[lo] * m_tiles;
+    GroupedTile t;
+    t.group = lo;
+    t.mtile = r / rt;
+    t.row0 = off[lo] + (r - t.mtile * rt) * N + part * width;
+    t.row_end = min(off[lo + 1], t.row0 + width);
+    constexpr int STEP = 16 * CG;
+    t.w = t.row_end > t.row0 ? (t.row_end - t.row0 + STEP - 1) / STEP * STEP : 0;
+    return t;
+  }
+};
 
 __device__ __forceinline__ uint64_t grouped_fma2(uint64_t a, uint64_t b, uint64_t c) {  // a * b + c, two fp32
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
+}
+__device__ __forceinline__ uint64_t pack_u64(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
+}
+
+// 16 lanes x 16 columns of tensor memory: thread T gets lanes T / 4 (r[0], r[1],
+// r[4], r[5]) and T / 4 + 8 (r[2], r[3], r[6], r[7]), columns 2 (T % 4) + {0, 1}
+// of the first (r[0..3]) and second (r[4..7]) eight.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// transpose of an 8 x 8 matrix of 16-bit values held two per thread (thread T:
+// row T / 4, columns 2 (T % 4) + {0, 1})
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// Writes an 8-row x 32-column piece of Y.  v[j]: fp32 pairs of columns T / 4 + 8 j
+// of W for rows 2 (T % 4) + {0, 1} of X.  Rounded to bf16 and transposed inside
+// the warp, each thread ends with 8 neighbouring columns of row T / 4: one
+// 16-byte store, 64 bytes of a row per four threads.
+__device__ __forceinline__ void grouped_store(const GroupedParams& p, const uint64_t (&v)[4], int row_base, int row_end,
+                                              int col_base, int lane) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(static_cast<uint32_t>(v[j])),
+                                                   __uint_as_float(static_cast<uint32_t>(v[j] >> 32)));
+    w[j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&t));
+  }
+  // thread q of four holds word q of each of the four 8-column blocks; it keeps
+  // its own block's: round r exchanges with thread q ^ r
+  const int q = lane & 3;
+  uint32_t o[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int j = q ^ r;
+    const uint32_t mine = j < 2 ? (j == 0 ? w[0] : w[1]) : (j == 2 ? w[2] : w[3]);
+    o[r] = r == 0 ? mine : __shfl_xor_sync(0xffffffffu, mine, r);  // word q ^ r of block q
+  }
+  uint32_t x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = q ^ j;
+    x[j] = r < 2 ? (r == 0 ? o[0] : o[1]) : (r == 2 ? o[2] : o[3]);
+  }
+  const int row = row_base + (lane >> 2);
+  const int col = col_base + q * 8;
+  if (row < row_end && col < p.m) {
+    uint16_t* y = p.Y + static_cast<int64_t>(row) * p.ldy + col;
+    if (col + 8 <= p.m) {
+      *reinterpret_cast<uint4*>(y) = make_uint4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < p.m) y[e] = static_cast<uint16_t>(x[e >> 1] >> ((e & 1) * 16));
+    }
+  }
 }
 
 template <bool FP8, int N, int MT, int CG>
@@ -150,7 +245,8 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   using C = GroupedCfg<N, MT, CG>;
   constexpr int STAGES = C::STAGES, HC = C::HC;
   constexpr int BK = FP8 ? 128 : 64;
-  constexpr uint32_t IDESC = FP8 ? make_idesc_e4m3(128 * CG, N, 1, 0) : make_idesc_bf16(128 * CG, N, 1, 0);
+  // the instructions' N is set per tile
+  constexpr uint32_t IDESC0 = FP8 ? make_idesc_e4m3(128 * CG, 0, 1, 0) : make_idesc_bf16(128 * CG, 0, 1, 0);
   // bytes between the k-steps of W in a stage (16 bf16 or 32 e4m3 rows of 128 bytes)
   constexpr uint32_t A_STEP = FP8 ? 4096 : 2048;
 
@@ -203,7 +299,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = pre[p.groups] * p.m_tiles;
+  const GroupedUnits<N, CG> units(p, off, pre, workers);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
@@ -212,10 +308,11 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
-      for (int tile = worker; ok && tile < total; tile += workers) {
-        const GroupedTile t = grouped_tile<N>(p, off, pre, tile);
+      for (int unit = worker; ok && unit < units.count; unit += workers) {
+        const GroupedTile t = units.get(unit);
+        if (t.w == 0) continue;
         const int f0 = (t.mtile * CG + static_cast<int>(rank)) * MT * 128;
-        const int row = t.row0 + static_cast<int>(rank) * C::X_ROWS;
+        const int row = t.row0 + static_cast<int>(rank) * (t.w / 2);  // half of a pair's rows
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer)) {
             ok = false;
@@ -265,7 +362,10 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       uint32_t phase = 0;
       uint32_t acc_i = 0;
       bool ok = true;
-      for (int tile = worker; ok && tile < total; tile += workers) {
+      for (int unit = worker; ok && unit < units.count; unit += workers) {
+        const int w = units.get(unit).w;
+        if (w == 0) continue;
+        const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w >> 3) << 17);
         for (int kb = 0; kb < p.num_kb; ++kb) {
           const uint32_t acc = acc_i & 1u;
           if (FP8 || kb == 0) {
@@ -291,11 +391,11 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
               const uint64_t ad = make_sw128_desc(a0 + mt * 16384 + kk * A_STEP, 8192, 1024);
               const uint32_t d = d_tmem + static_cast<uint32_t>(mt * N);
               if (CG == 2) {
-                if (FP8) umma_e4m3_pair(d, ad, xd, IDESC, add);
-                else umma_bf16_pair(d, ad, xd, IDESC, add);
+                if (FP8) umma_e4m3_pair(d, ad, xd, idesc, add);
+                else umma_bf16_pair(d, ad, xd, idesc, add);
               } else {
-                if (FP8) umma_e4m3(d, ad, xd, IDESC, add);
-                else umma_bf16(d, ad, xd, IDESC, add);
+                if (FP8) umma_e4m3(d, ad, xd, idesc, add);
+                else umma_bf16(d, ad, xd, idesc, add);
               }
             }
           }
@@ -321,19 +421,17 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int quarter = warp & 3;
-    const int half = (warp - 4) >> 2;
-    // this thread's accumulator columns [half * HC, half * HC + HC): rows of X
-    // row_of(i), columns of W in 128-column tile mt_of(i)
-    const int mt0 = HC >= N ? half * (HC / N) : 0;
-    const int r0 = HC >= N ? 0 : half * HC;
-    auto mt_of = [&](int i) { return HC >= N ? mt0 + i / N : 0; };
-    auto row_of = [&](int i) { return HC >= N ? i % N : r0 + i; };
+    const int quarter = warp & 3;         // lanes of tensor memory a warp may read
+    const int half = (warp - 2) >> 2;
+    // this thread's accumulator columns [half * HC, half * HC + HC): rows r_of(i)
+    // of the tile, columns of W in its 128-column tile mt_of(i)
+    auto mt_of = [&](int i) { return HC >= N ? half * (HC / N) + i / N : 0; };
+    auto r_of = [&](int i) { return HC >= N ? i % N : half * HC + i; };
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HC);
     const uint32_t tempty_even = CG == 2 ? map_shared_rank(smem_u32(&tempty[0]), 0u) : 0u;
-    float* my_scale = sScale + (warp - 4) * 2 * HC;
+    float* my_scale = sScale + (warp - 2) * 2 * HC;
     uint32_t acc_i = 0;
     bool ok = true;
     auto release = [&](uint32_t acc) {  // this warp has read the accumulator
@@ -344,72 +442,92 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         else mbar_arrive_cluster(tempty_even + 8u * acc);
       }
     };
-    for (int tile = worker; ok && tile < total; tile += workers) {
-      const GroupedTile t = grouped_tile<N>(p, off, pre, tile);
+    for (int unit = worker; ok && unit < units.count; unit += workers) {
+      const GroupedTile t = units.get(unit);
+      if (t.w == 0) continue;
       const int mblock0 = (t.mtile * CG + static_cast<int>(rank)) * MT;  // first 128-column tile
-      auto store = [&](int i, float v) {
-        const int row = t.row0 + row_of(i);
-        const int f = (mblock0 + mt_of(i)) * 128 + quarter * 32 + lane;
-        if (row < t.row_end && f < p.m)
-          reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<int64_t>(row) * p.ldy + f] = __float2bfloat16_rn(v);
-      };
       if (FP8) {
-        uint64_t sum[HC / 2];
+        // sum[g][j]: columns T / 4 + 8 j of the warp's 32, rows 8 g + 2 (T % 4) + {0, 1}
+        uint64_t sum[HC / 8][4];
 #pragma unroll
-        for (int i = 0; i < HC / 2; ++i) sum[i] = 0;
+        for (int g = 0; g < HC / 8; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[g][j] = 0;
+        // scales of this warp's HC rows (lane, lane + 32, ...) and of the weight
+        // blocks, loaded one block ahead
+        float nx[HC / 32], nw[HC / 32];
+        auto load_scales = [&](int kb) {
+#pragma unroll
+          for (int i = 0; i < HC / 32; ++i) {
+            const int row = t.row0 + r_of(i * 32 + lane);
+            const int mb = mblock0 + mt_of(i * 32 + lane);
+            const bool there = row < t.row_end && mb < p.sw_cols;
+            nx[i] = there ? __ldg(p.sx + kb * p.lds + row) : 0.f;
+            nw[i] = there ? __ldg(p.sw + (static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb) : 0.f;
+          }
+        };
+        load_scales(0);
         for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
           const uint32_t acc = acc_i & 1u;
           float* sc = my_scale + acc * HC;
 #pragma unroll
-          for (int i = 0; i < HC / 32; ++i) {
-            const int c = i * 32 + lane;
-            const int row = t.row0 + row_of(c);
-            const int mb = mblock0 + mt_of(c);
-            float v = 0.f;
-            if (row < t.row_end && mb < p.sw_cols)
-              v = __ldg(p.sx + kb * p.lds + row) *
-                  __ldg(p.sw + (static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb);
-            sc[c] = v;
-          }
+          for (int i = 0; i < HC / 32; ++i) sc[i * 32 + lane] = nx[i] * nw[i];
           __syncwarp();
+          if (kb + 1 < p.num_kb) load_scales(kb + 1);
           if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t base = lane_base + acc * C::COLS;
+          // two 8-column groups at a time, the next two on their way
+          uint32_t r[2][2][8];
+          tmem_ld_16x16(base, r[0][0]);
+          tmem_ld_16x16(base + (16u << 16), r[0][1]);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < HC / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + acc * C::COLS + c * 32, r);
-            tmem_ld_wait();
-            if (c == HC / 32 - 1) release(acc);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(sc + c * 32 + e);
-              uint64_t& a = sum[(c * 32 + e) / 2];
-              uint64_t& b = sum[(c * 32 + e) / 2 + 1];
-              a = grouped_fma2(static_cast<uint64_t>(r[e]) | (static_cast<uint64_t>(r[e + 1]) << 32), s2.x, a);
-              b = grouped_fma2(static_cast<uint64_t>(r[e + 2]) | (static_cast<uint64_t>(r[e + 3]) << 32), s2.y, b);
+          for (int c = 0; c < HC / 16; ++c) {
+            if (c + 1 < HC / 16) {
+              tmem_ld_16x16(base + (c + 1) * 16, r[(c + 1) & 1][0]);
+              tmem_ld_16x16(base + (c + 1) * 16 + (16u << 16), r[(c + 1) & 1][1]);
             }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + c * 16 + g * 8 + 2 * (lane & 3));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t* v = &r[c & 1][j >> 1][g * 4 + (j & 1) * 2];
+                sum[2 * c + g][j] = grouped_fma2(pack_u64(v[0], v[1]), s2, sum[2 * c + g][j]);
+              }
+            }
+            if (c + 1 < HC / 16) tmem_ld_wait();
+            if (c + 2 == HC / 16 || HC == 16) release(acc);
           }
         }
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < HC / 2; ++i) {
-          store(2 * i, __uint_as_float(static_cast<uint32_t>(sum[i])));
-          store(2 * i + 1, __uint_as_float(static_cast<uint32_t>(sum[i] >> 32)));
-        }
+        for (int g = 0; g < HC / 8; ++g)
+          grouped_store(p, sum[g], t.row0 + r_of(g * 8), t.row_end, (mblock0 + mt_of(g * 8)) * 128 + quarter * 32, lane);
       } else {
         const uint32_t acc = acc_i & 1u;
         if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue, 64)) break;
         tc_fence_after();
-        for (int c = 0; c < HC / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(lane_base + acc * C::COLS + c * 32, r);
+        const uint32_t base = lane_base + acc * C::COLS;
+#pragma unroll 4
+        for (int c = 0; c < HC / 16; ++c) {
+          uint32_t r[2][8];
+          tmem_ld_16x16(base + c * 16, r[0]);
+          tmem_ld_16x16(base + c * 16 + (16u << 16), r[1]);
           tmem_ld_wait();
-          if (c == HC / 32 - 1) release(acc);
+          if (c == HC / 16 - 1) release(acc);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) store(c * 32 + e, __uint_as_float(r[e]));
+          for (int g = 0; g < 2; ++g) {
+            uint64_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = pack_u64(r[j >> 1][g * 4 + (j & 1) * 2], r[j >> 1][g * 4 + (j & 1) * 2 + 1]);
+            grouped_store(p, v, t.row0 + r_of(c * 16 + g * 8), t.row_end,
+                          (mblock0 + mt_of(c * 16 + g * 8)) * 128 + quarter * 32, lane);
+          }
         }
         ++acc_i;
       }
