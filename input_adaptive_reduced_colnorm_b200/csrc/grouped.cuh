@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         for (int kb = 0; kb < p.num_kb; ++kb) {
           const uint32_t acc = acc_i & 1u;
           if (FP8 || kb == 0) {
-            if (!mbar_wait(&tempty[acc], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, CG == 2)) {
+            if (!mbar_wait(&tempty[acc], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0,
+                           CG == 2 ? kMbarClusterRelaxed : kMbarCta)) {
               ok = false;
               break;
             }
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&tempty[acc]);
-        else mbar_arrive_cluster(tempty_even + 8u * acc);
+        else mbar_arrive_cluster_relaxed(tempty_even + 8u * acc);
       }
     };
     for (int unit = worker; ok && unit < units.count; unit += workers) {

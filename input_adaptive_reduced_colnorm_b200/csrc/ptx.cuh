@@ -91,6 +91,23 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// try_wait with cluster scope and no ordering of other memory operations, for
+// barriers that only hand over tensor memory (ordered by the tcgen05 fences).
+__device__ __forceinline__ bool mbar_try_wait_cluster_relaxed(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Which other memory operations a wait orders.
+enum MbarScope : int { kMbarCta = 0, kMbarCluster = 1, kMbarClusterRelaxed = 2 };
+
 // Wait for the phase of ``bar`` with parity ``parity`` to complete.  Gives up
 // after ``limit_ns`` (kWaitTimeoutNs unless a test hook asks for less) without
 // progress, or as soon as *abort is set by another role of the same CTA; on a
@@ -99,10 +116,14 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 // warps waiting for a finished accumulator) then leave the issue slots to the
 // warps that are moving data.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t code,
-                                          uint32_t sleep_ns = 0, bool cluster_scope = false,
+                                          uint32_t sleep_ns = 0, int scope = kMbarCta,
                                           uint64_t limit_ns = kWaitTimeoutNs) {
   const uint32_t a = smem_u32(bar);
-  auto poll = [&]() { return cluster_scope ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
+  auto poll = [&]() {
+    return scope == kMbarClusterRelaxed ? mbar_try_wait_cluster_relaxed(a, parity)
+           : scope == kMbarCluster      ? mbar_try_wait_cluster(a, parity)
+                                        : mbar_try_wait(a, parity);
+  };
   if (poll()) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -412,6 +433,10 @@ __device__ __forceinline__ uint32_t map_shared_rank(uint32_t addr, uint32_t rank
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+// The same without ordering other memory operations (see kMbarClusterRelaxed).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 __device__ __forceinline__ double ld_shared_cluster_f64(uint32_t addr) {
   double v;

@@ -25,6 +25,7 @@
 #include "decode_select.cuh"
 #include "quantize.cuh"
 #include "grouped.cuh"
+#include "grouped_fp8.cuh"
 
 using namespace rmm;
 
@@ -1951,8 +1952,9 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   p.m_tiles = static_cast<int>(ceil_div(c.m, CG * MT * 128));
   // row tiles: at most n / N whole ones and a partial one per group
   const int64_t row_tiles = ceil_div(c.n, N) + std::min<int64_t>(c.groups - 1, c.n);
-  if (row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
-  const int64_t workers = std::min<int64_t>(row_tiles * p.m_tiles, std::max(1, num_sms() / CG));
+  // (a tile of the last wave may be cut into up to eight)
+  if (8 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
+  const int64_t workers = std::min<int64_t>((N >= 128 ? N / 32 : 1) * row_tiles * p.m_tiles, std::max(1, num_sms() / CG));
   const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
   auto kern = grouped_kernel<FP8, N, MT, CG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1964,6 +1966,25 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   return RMM_OK;
 }
 
+rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
+  CUtensorMap tw, tx;
+  if (rmm_status st = make_tmaps_grouped(&tw, &tx, true, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx, 128))
+    return st;
+  GroupedParams p = c.p;
+  p.num_kb = static_cast<int>(ceil_div(c.d, 128));
+  p.m_tiles = static_cast<int>(ceil_div(c.m, 256));
+  const int64_t row_tiles = ceil_div(c.n, 256) + std::min<int64_t>(c.groups - 1, c.n);
+  if (4 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
+  const int64_t workers = std::min<int64_t>(4 * row_tiles * p.m_tiles, std::max(1, num_sms() / 2));
+  const int smem = GroupedFp8Cfg::smem_bytes(static_cast<int>(c.groups));
+  cudaError_t e = cudaFuncSetAttribute(grouped_fp8_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
+  e = launch_cluster(grouped_fp8_rows_kernel, dim3(static_cast<unsigned>(workers * 2)), dim3(GroupedFp8Cfg::THREADS), smem, 2,
+                     s, tw, tx, p);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
+  return RMM_OK;
+}
+
 template <bool FP8>
 rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   const int64_t rows = ceil_div(c.n, c.groups);  // of an average group
@@ -1971,7 +1992,8 @@ rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   if (rows <= 32) return launch_grouped_t<FP8, 32, 4, 1>(c, s);
   if (rows <= 64) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
   if (rows <= 128) return launch_grouped_t<FP8, 128, 2, 1>(c, s);
-  return launch_grouped_t<FP8, 256, 1, 2>(c, s);
+  if (FP8) return launch_grouped_fp8_rows(c, s);
+  return launch_grouped_t<false, 256, 1, 2>(c, s);
 }
 
 // Checks shared by the product calls; `unit` = elements of 16 bytes.
