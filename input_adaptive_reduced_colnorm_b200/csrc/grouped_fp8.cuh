@@ -24,6 +24,11 @@ struct GroupedFp8Cfg {
   static constexpr int W_BYTES = 128 * 128;  // its 128 of the 256 columns
   static constexpr int STAGES = 6;
   static constexpr int THREADS = 384;
+  // registers per thread at launch, and the split after the set-up: 128 sums and
+  // two 32-column loads in flight per epilogue thread (the host checks that the
+  // kernel was compiled to LAUNCH_REGS, on which the split draws)
+  static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 56, EPI_REGS = 224;
+  static_assert(OTHER_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "three warpgroups share what was launched");
   static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + 256 + (2 * groups + 2) * 4; }
   static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier area");
 };
@@ -116,6 +121,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const GroupedFp8Units units(p, off, pre, workers);
 
+  if (warp < 4) set_max_regs_down<C::OTHER_REGS>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     if (lane == 0) {
@@ -197,6 +203,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
+    set_max_regs_up<C::EPI_REGS>();
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tempty_even = map_shared_rank(smem_u32(&tempty[0]), 0u);
     uint32_t acc_i = 0;
@@ -213,15 +220,15 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       uint64_t sum[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sum[i] = 0;
-      float nx = __ldg(sx), nw = __ldg(sw);  // scales, loaded one block ahead
+      float nx = ldg_f32_pinned(sx), nw = ldg_f32_pinned(sw);  // scales, loaded one block ahead
       for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
         const uint32_t acc = acc_i & 1u;
         const float s = nx * nw;
         if (kb + 1 < p.num_kb) {
           sx += p.lds;
           sw += p.sw_cols;
-          nx = __ldg(sx);
-          nw = __ldg(sw);
+          nx = ldg_f32_pinned(sx);
+          nw = ldg_f32_pinned(sw);
         }
         const uint64_t s2 = pack_u64(__float_as_uint(s), __float_as_uint(s));
         if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) {
@@ -229,21 +236,26 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           break;
         }
         tc_fence_after();
+        // 32 columns at a time, the next 32 on their way (a narrow piece reads past
+        // its columns, inside the accumulator; those sums are not stored)
+        uint32_t r[2][32];
+        tmem_ld32(base + acc * 256, r[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if (c * 32 < hw) {
-            uint32_t r[32];
-            tmem_ld32(base + acc * 256 + c * 32, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sum[c * 16 + e] = grouped_fma2(pack_u64(r[2 * e], r[2 * e + 1]), s2, sum[c * 16 + e]);
+          tmem_ld_wait();
+          if (c < 3) {
+            tmem_ld32(base + acc * 256 + (c + 1) * 32, r[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive(&tempty[acc]);
+              else mbar_arrive_cluster_relaxed(tempty_even + 8u * acc);
+            }
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(&tempty[acc]);
-          else mbar_arrive_cluster_relaxed(tempty_even + 8u * acc);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            sum[c * 16 + e] = grouped_fma2(pack_u64(r[c & 1][2 * e], r[c & 1][2 * e + 1]), s2, sum[c * 16 + e]);
         }
       }
       if (!ok) break;

@@ -444,7 +444,25 @@ __device__ __forceinline__ double ld_shared_cluster_f64(uint32_t addr) {
   return v;
 }
 
+// ---------------------------------------------------------------- registers
+// Hands registers of this warpgroup back to the block, or takes more (waits until
+// the block's launch total has them).  All warps of the warpgroup execute it.
+template <int R>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 // ---------------------------------------------------------------- misc loads
+// A load that stays where it is written (a plain one may be moved down to its use).
+__device__ __forceinline__ float ldg_f32_pinned(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

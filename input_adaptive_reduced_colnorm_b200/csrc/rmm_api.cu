@@ -1979,6 +1979,14 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   const int smem = GroupedFp8Cfg::smem_bytes(static_cast<int>(c.groups));
   cudaError_t e = cudaFuncSetAttribute(grouped_fp8_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
+  // the kernel moves registers between its warpgroups: never launch it with fewer
+  // than the split needs, it would wait for them for good
+  static const int regs = [] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, grouped_fp8_rows_kernel) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != GroupedFp8Cfg::LAUNCH_REGS)
+    return fail(RMM_ERR_CUDA, "grouped fp8 kernel compiled to %d registers, not %d", regs, GroupedFp8Cfg::LAUNCH_REGS);
   e = launch_cluster(grouped_fp8_rows_kernel, dim3(static_cast<unsigned>(workers * 2)), dim3(GroupedFp8Cfg::THREADS), smem, 2,
                      s, tw, tx, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
