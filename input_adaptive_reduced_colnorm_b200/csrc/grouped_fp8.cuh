@@ -11,8 +11,15 @@
 // swapped form needs reads half as fast, 546 cycles).  What it costs is a group's
 // last tile, 256 rows however few are left.
 //
+// A block's product is issued as two of half the columns with barriers of their
+// own, so that the two epilogue warps of a scheduler work out of step (one loads
+// and waits while the other multiplies); each takes the next block's first columns
+// out of tensor memory before it adds the last ones of this block.
+//
 // Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer (even CTA), warps
-// 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 and one half of the columns.
+// 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two products.
+// The columns of product h are two runs, one from each CTA's half of the tile:
+// [h w / 4, (h + 1) w / 4) and w / 2 further, w the tile's columns.
 // The tiles of a partial last wave are cut along W into 128- or 64-column pieces.
 #pragma once
 #include "grouped.cuh"
@@ -30,7 +37,7 @@ struct GroupedFp8Cfg {
   static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 56, EPI_REGS = 224;
   static_assert(OTHER_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "three warpgroups share what was launched");
   static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + 256 + (2 * groups + 2) * 4; }
-  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier area");
+  static_assert(8 * (2 * STAGES + 9) + 8 <= 256, "barrier area");
 };
 
 struct GroupedFp8Units {
@@ -84,14 +91,14 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sW + STAGES * C::W_BYTES);  // used in the even CTA
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;  // used in the even CTA
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + 4;  // used in the even CTA; both [accumulator][half]
+  uint64_t* drain = tempty + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   int* pre = off + p.groups + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues the MMAs
   const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
   if (threadIdx.x == 0) {
@@ -99,9 +106,9 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < 4; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 16);  // eight epilogue warps of each CTA
+      mbar_init(&tempty[a], 8);  // four epilogue warps of each CTA
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -165,39 +172,54 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    // (the warp runs the loop together and elects the issuing lane, so that the
+    // descriptors stay in uniform registers)
+    if (rank == 0) {
+      const uint64_t xd0 = make_sw128_desc(smem_u32(sX), 16, 1024), wd0 = make_sw128_desc(smem_u32(sW), 16384, 1024);
       int stage = 0;
       uint32_t phase = 0, acc_i = 0;
       bool ok = true;
       for (int unit = worker; ok && unit < units.count; unit += workers) {
-        const uint32_t idesc = make_idesc_e4m3(256, 0, 0, 1) | (static_cast<uint32_t>(units.get(unit).w >> 3) << 17);
+        const int w = units.get(unit).w;
+        const uint32_t idesc = make_idesc_e4m3(256, 0, 0, 1) | (static_cast<uint32_t>(w >> 4) << 17);  // N = w / 2
         for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
           const uint32_t acc = acc_i & 1u;
-          if (!mbar_wait(&tempty[acc], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed) ||
-              !mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t x0 = smem_u32(sX + stage * C::X_BYTES);
-          const uint32_t w0 = smem_u32(sW + stage * C::W_BYTES);
+          const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
+          const uint64_t wd = wd0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_e4m3_pair(tmem_base + acc * 256, make_sw128_desc(x0 + kk * 32, 16, 1024),
-                           make_sw128_desc(w0 + kk * 4096, 16384, 1024), idesc, kk != 0 ? 1u : 0u);
-          umma_commit_pair(&empty[stage], 0x3);
-          umma_commit_pair(&tfull[acc], 0x3);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t buf = acc * 2 + h;
+            bool go = mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed);
+            if (h == 0) go = go && mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma);
+            if (!__all_sync(0xffffffffu, go)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t wh = wd + static_cast<uint64_t>((h * (w >> 2)) >> 4);  // w / 4 columns of each CTA
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_e4m3_pair(tmem_base + buf * 128, xd + static_cast<uint64_t>(kk * (32 >> 4)),
+                               wh + static_cast<uint64_t>(kk * (4096 >> 4)), idesc, kk != 0 ? 1u : 0u);
+              if (h == 1) umma_commit_pair(&empty[stage], 0x3);
+              umma_commit_pair(&tfull[buf], 0x3);
+            }
+          }
+          if (!ok) break;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
+      if (lane == 0) {
       // every MMA issued by this thread is complete once `drain` flips
       umma_commit_pair(drain, 0x1);
       const uint32_t a = smem_u32(drain);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+      }
       }
     }
     __syncwarp();
@@ -211,74 +233,93 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     for (int unit = worker; ok && unit < units.count; unit += workers) {
       const GroupedTile t = units.get(unit);
       const int row = t.row0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-      const int hw = t.w / 2;                    // columns of this thread: 128, 64 or 32
-      const int col0 = t.mtile + half * hw;      // they lie in one 128-column block of scales
-      const bool row_ok = row < t.row_end, cols_ok = col0 < p.m;
+      const int run = t.w / 4;                   // columns of each of this thread's two runs
+      const int col0 = t.mtile + half * run;     // the first run's; the second starts t.w / 2 further
+      const bool row_ok = row < t.row_end;
       const float* sx = p.sx + (row_ok ? row : 0);
-      const float* sw = p.sw + static_cast<int64_t>(t.group) * p.num_kb * p.sw_cols + (cols_ok ? col0 / 128 : 0);
-      const uint32_t base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * hw);
-      uint64_t sum[64];
+      const float* sw = p.sw + static_cast<int64_t>(t.group) * p.num_kb * p.sw_cols;
+      // a run lies in one 128-column block of scales (past the edge: any)
+      const int sb0 = min(col0 / 128, p.sw_cols - 1), sb1 = min((col0 + t.w / 2) / 128, p.sw_cols - 1);
+      const uint32_t base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+      float sum[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = 0;
-      float nx = ldg_f32_pinned(sx), nw = ldg_f32_pinned(sw);  // scales, loaded one block ahead
-      for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
-        const uint32_t acc = acc_i & 1u;
-        const float s = nx * nw;
-        if (kb + 1 < p.num_kb) {
+      for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+      // scales of the block being added and of the next two
+      float x1 = ldg_f32_pinned(sx), u1 = ldg_f32_pinned(sw + sb0), v1 = ldg_f32_pinned(sw + sb1);
+      float s0 = x1 * u1, s1 = x1 * v1;
+      auto next_scales = [&](int kb, float& x, float& u, float& v) {
+        if (kb < p.num_kb) {
           sx += p.lds;
           sw += p.sw_cols;
-          nx = ldg_f32_pinned(sx);
-          nw = ldg_f32_pinned(sw);
+          x = ldg_f32_pinned(sx);
+          u = ldg_f32_pinned(sw + sb0);
+          v = ldg_f32_pinned(sw + sb1);
         }
-        const uint64_t s2 = pack_u64(__float_as_uint(s), __float_as_uint(s));
-        if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        // 32 columns at a time, the next 32 on their way (a narrow piece reads past
-        // its columns, inside the accumulator; those sums are not stored)
-        uint32_t r[2][32];
-        tmem_ld32(base + acc * 256, r[0]);
+      };
+      next_scales(1, x1, u1, v1);
+      uint32_t r[2][16];
+      ok = mbar_wait(&tfull[(acc_i & 1u) * 2 + half], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld16(base + (acc_i & 1u) * 256, r[0]);
+      for (int kb = 0; ok && kb < p.num_kb; ++kb) {
+        const uint32_t acc = acc_i & 1u;
+        ++acc_i;
+        float x2 = 0.f, u2 = 0.f, v2 = 0.f;
+        next_scales(kb + 2, x2, u2, v2);
+        // 16 columns at a time, the next 16 on their way (a narrow piece reads past
+        // its columns, inside the accumulator; those sums are not stored).  The
+        // loads stand outside every branch, and the additions keep their place:
+        // left to itself the compiler moved them past the waits, 1.2x the time.
+        uint64_t* next_full = &tfull[(acc ^ 1u) * 2 + half];
+        bool ready = true;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 8; ++c) {
           tmem_ld_wait();
-          if (c < 3) {
-            tmem_ld32(base + acc * 256 + (c + 1) * 32, r[(c + 1) & 1]);
+          if (c < 7) {
+            tmem_ld16(base + acc * 256 + (c + 1) * 16, r[(c + 1) & 1]);
+            // (asked early: the answer takes about as long as the additions)
+            if (c == 5) ready = kb + 1 == p.num_kb || mbar_try_wait(smem_u32(next_full), (acc_i >> 1) & 1u);
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if (rank == 0) mbar_arrive(&tempty[acc]);
-              else mbar_arrive_cluster_relaxed(tempty_even + 8u * acc);
-            }
+            if (elect_one()) mbar_arrive_cluster_relaxed(tempty_even + 8u * (acc * 2 + half));
+            if (!ready) ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
+            tc_fence_after();
+            tmem_ld16(base + (acc ^ 1u) * 256, r[0]);  // (after the last block: not used)
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            sum[c * 16 + e] = grouped_fma2(pack_u64(r[c & 1][2 * e], r[c & 1][2 * e + 1]), s2, sum[c * 16 + e]);
+          for (int e = 0; e < 16; ++e) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), c < 4 ? s0 : s1);
         }
+        s0 = x1 * u1;
+        s1 = x1 * v1;
+        x1 = x2;
+        u1 = u2;
+        v1 = v2;
       }
+      tmem_ld_wait();
       if (!ok) break;
       if (row_ok) {
-        uint16_t* y = p.Y + static_cast<int64_t>(row) * p.ldy + col0;
+        uint16_t* y = p.Y + static_cast<int64_t>(row) * p.ldy;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const int left = min(hw, p.m - col0) - c * 8;  // columns of this 16-byte piece that exist
-          if (left <= 0) break;
+          // accumulator columns 8 c .. 8 c + 7
+          if (c * 8 >= 2 * run) break;
+          const int second = c * 8 >= run ? 1 : 0;
+          const int col = col0 + second * (t.w / 2 - run) + c * 8;
+          const int left = p.m - col;  // columns of this 16-byte piece that exist
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint64_t v = sum[c * 4 + e];
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(static_cast<uint32_t>(v)),
-                                                           __uint_as_float(static_cast<uint32_t>(v >> 32)));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(sum[c * 8 + 2 * e], sum[c * 8 + 2 * e + 1]);
             w[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
           if (left >= 8) {
-            *reinterpret_cast<uint4*>(y + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(y + col) = make_uint4(w[0], w[1], w[2], w[3]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (e < left) y[c * 8 + e] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
+              if (e < left) y[col + e] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
           }
         }
       }

@@ -444,6 +444,22 @@ __device__ __forceinline__ double ld_shared_cluster_f64(uint32_t addr) {
   return v;
 }
 
+// c += a * b that stays where it is written.
+__device__ __forceinline__ void fma_pinned(float& c, float a, float b) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(c) : "f"(a), "f"(b));
+}
+
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- registers
 // Hands registers of this warpgroup back to the block, or takes more (waits until
 // the block's launch total has them).  All warps of the warpgroup execute it.
