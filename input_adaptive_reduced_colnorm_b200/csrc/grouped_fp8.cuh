@@ -16,8 +16,8 @@
 // and waits while the other multiplies); each takes the next block's first columns
 // out of tensor memory before it adds the last ones of this block.
 //
-// Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer (even CTA), warps
-// 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two products.
+// Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers (even CTA),
+// one for each product, warp 3 the group bounds, warps 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two products.
 // The columns of product h are two runs, one from each CTA's half of the tile:
 // [h w / 4, (h + 1) w / 4) and w / 2 further, w the tile's columns.
 // The tiles of a partial last wave are cut along W into 128- or 64-column pieces.
@@ -39,6 +39,34 @@ struct GroupedFp8Cfg {
   static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + 256 + (2 * groups + 2) * 4; }
   static_assert(8 * (2 * STAGES + 9) + 8 <= 256, "barrier area");
 };
+
+// sum[0..15] += v[0..15] * s between the question whether a phase of a barrier is
+// complete and its answer, which takes some 200 cycles even when it is.
+__device__ __forceinline__ uint32_t test_wait_fma16(uint32_t bar, uint32_t parity, float* sum, const uint32_t (&v)[16], float s) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%17], %18;\n\t"
+      "fma.rn.f32 %1, %19, %35, %1;\n\tfma.rn.f32 %2, %20, %35, %2;\n\t"
+      "fma.rn.f32 %3, %21, %35, %3;\n\tfma.rn.f32 %4, %22, %35, %4;\n\t"
+      "fma.rn.f32 %5, %23, %35, %5;\n\tfma.rn.f32 %6, %24, %35, %6;\n\t"
+      "fma.rn.f32 %7, %25, %35, %7;\n\tfma.rn.f32 %8, %26, %35, %8;\n\t"
+      "fma.rn.f32 %9, %27, %35, %9;\n\tfma.rn.f32 %10, %28, %35, %10;\n\t"
+      "fma.rn.f32 %11, %29, %35, %11;\n\tfma.rn.f32 %12, %30, %35, %12;\n\t"
+      "fma.rn.f32 %13, %31, %35, %13;\n\tfma.rn.f32 %14, %32, %35, %14;\n\t"
+      "fma.rn.f32 %15, %33, %35, %15;\n\tfma.rn.f32 %16, %34, %35, %16;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok), "+f"(sum[0]), "+f"(sum[1]), "+f"(sum[2]), "+f"(sum[3]), "+f"(sum[4]), "+f"(sum[5]), "+f"(sum[6]),
+        "+f"(sum[7]), "+f"(sum[8]), "+f"(sum[9]), "+f"(sum[10]), "+f"(sum[11]), "+f"(sum[12]), "+f"(sum[13]),
+        "+f"(sum[14]), "+f"(sum[15])
+      : "r"(bar), "r"(parity), "f"(__uint_as_float(v[0])), "f"(__uint_as_float(v[1])), "f"(__uint_as_float(v[2])),
+        "f"(__uint_as_float(v[3])), "f"(__uint_as_float(v[4])), "f"(__uint_as_float(v[5])), "f"(__uint_as_float(v[6])),
+        "f"(__uint_as_float(v[7])), "f"(__uint_as_float(v[8])), "f"(__uint_as_float(v[9])), "f"(__uint_as_float(v[10])),
+        "f"(__uint_as_float(v[11])), "f"(__uint_as_float(v[12])), "f"(__uint_as_float(v[13])),
+        "f"(__uint_as_float(v[14])), "f"(__uint_as_float(v[15])), "f"(s)
+      : "memory");
+  return ok;
+}
 
 struct GroupedFp8Units {
   const int *off, *pre;
@@ -104,13 +132,13 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // both issuers
     }
     for (int a = 0; a < 4; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 8);  // four epilogue warps of each CTA
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -121,7 +149,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     tmem_relinquish_pair();
   }
   wait_prior_kernels();  // bounds, operands and the output are touched only after this
-  if (warp == 2) grouped_bounds<256>(p, off, pre, lane);
+  if (warp == 3) grouped_bounds<256>(p, off, pre, lane);
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
   tc_fence_after();
@@ -170,11 +198,14 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (even CTA)
-    // (the warp runs the loop together and elects the issuing lane, so that the
-    // descriptors stay in uniform registers)
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMA issuers (even CTA)
+    // warp 1 issues the product of the first half of the columns, warp 2 that of the
+    // second (one warp's waits for both, 3 of about 100 cycles a block, left the
+    // tensor cores idle).  The warp runs the loop together and elects the issuing
+    // lane, so that the descriptors stay in uniform registers.
     if (rank == 0) {
+      const int h = warp - 1;
       const uint64_t xd0 = make_sw128_desc(smem_u32(sX), 16, 1024), wd0 = make_sw128_desc(smem_u32(sW), 16384, 1024);
       int stage = 0;
       uint32_t phase = 0, acc_i = 0;
@@ -183,43 +214,39 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
         const int w = units.get(unit).w;
         const uint32_t idesc = make_idesc_e4m3(256, 0, 0, 1) | (static_cast<uint32_t>(w >> 4) << 17);  // N = w / 2
         for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
-          const uint32_t acc = acc_i & 1u;
-          const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
-          const uint64_t wd = wd0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4));
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t buf = acc * 2 + h;
-            bool go = mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed);
-            if (h == 0) go = go && mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma);
-            if (!__all_sync(0xffffffffu, go)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t wh = wd + static_cast<uint64_t>((h * (w >> 2)) >> 4);  // w / 4 columns of each CTA
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_e4m3_pair(tmem_base + buf * 128, xd + static_cast<uint64_t>(kk * (32 >> 4)),
-                               wh + static_cast<uint64_t>(kk * (4096 >> 4)), idesc, kk != 0 ? 1u : 0u);
-              if (h == 1) umma_commit_pair(&empty[stage], 0x3);
-              umma_commit_pair(&tfull[buf], 0x3);
-            }
+          const uint32_t buf = (acc_i & 1u) * 2 + h;
+          const bool go =
+              mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed) &&
+              mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma);
+          if (!__all_sync(0xffffffffu, go)) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
+            // w / 4 columns of each CTA
+            const uint64_t wd = wd0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4)) + static_cast<uint64_t>((h * (w >> 2)) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_e4m3_pair(tmem_base + buf * 128, xd + static_cast<uint64_t>(kk * (32 >> 4)),
+                             wd + static_cast<uint64_t>(kk * (4096 >> 4)), idesc, kk != 0 ? 1u : 0u);
+            umma_commit_pair(&tfull[buf], 0x3);
+            umma_commit_pair(&empty[stage], 0x3);
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (lane == 0) {
-      // every MMA issued by this thread is complete once `drain` flips
-      umma_commit_pair(drain, 0x1);
-      const uint32_t a = smem_u32(drain);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
-      }
+      if (elect_one()) {
+        // every MMA issued by this warp is complete once `drain` flips
+        umma_commit_pair(drain, 0x1);
+        const uint32_t a = smem_u32(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+        }
       }
     }
     __syncwarp();
@@ -244,19 +271,18 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
-      // scales of the block being added and of the next two
-      float x1 = ldg_f32_pinned(sx), u1 = ldg_f32_pinned(sw + sb0), v1 = ldg_f32_pinned(sw + sb1);
-      float s0 = x1 * u1, s1 = x1 * v1;
-      auto next_scales = [&](int kb, float& x, float& u, float& v) {
-        if (kb < p.num_kb) {
-          sx += p.lds;
-          sw += p.sw_cols;
-          x = ldg_f32_pinned(sx);
-          u = ldg_f32_pinned(sw + sb0);
-          v = ldg_f32_pinned(sw + sb1);
-        }
+      // scales of the block being added and of the next two (past the last block: its own again)
+      const int last = p.num_kb - 1;
+      auto load_scales = [&](int kb, float& x, float& u, float& v) {
+        const int64_t b = min(kb, last);
+        x = ldg_f32_pinned(sx + b * p.lds);
+        u = ldg_f32_pinned(sw + sb0 + b * p.sw_cols);
+        v = ldg_f32_pinned(sw + sb1 + b * p.sw_cols);
       };
-      next_scales(1, x1, u1, v1);
+      float x1, u1, v1;
+      load_scales(0, x1, u1, v1);
+      float s0 = x1 * u1, s1 = x1 * v1;
+      load_scales(1, x1, u1, v1);
       uint32_t r[2][16];
       ok = mbar_wait(&tfull[(acc_i & 1u) * 2 + half], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
       if (!ok) break;
@@ -265,31 +291,32 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       for (int kb = 0; ok && kb < p.num_kb; ++kb) {
         const uint32_t acc = acc_i & 1u;
         ++acc_i;
-        float x2 = 0.f, u2 = 0.f, v2 = 0.f;
-        next_scales(kb + 2, x2, u2, v2);
+        float x2, u2, v2;
+        load_scales(kb + 2, x2, u2, v2);
         // 16 columns at a time, the next 16 on their way (a narrow piece reads past
         // its columns, inside the accumulator; those sums are not stored).  The
         // loads stand outside every branch, and the additions keep their place:
         // left to itself the compiler moved them past the waits, 1.2x the time.
         uint64_t* next_full = &tfull[(acc ^ 1u) * 2 + half];
-        bool ready = true;
+        uint32_t ready = 0;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           tmem_ld_wait();
           if (c < 7) {
             tmem_ld16(base + acc * 256 + (c + 1) * 16, r[(c + 1) & 1]);
-            // (asked early: the answer takes about as long as the additions)
-            if (c == 5) ready = kb + 1 == p.num_kb || mbar_try_wait(smem_u32(next_full), (acc_i >> 1) & 1u);
           } else {
             tc_fence_before();
             __syncwarp();
             if (elect_one()) mbar_arrive_cluster_relaxed(tempty_even + 8u * (acc * 2 + half));
-            if (!ready) ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
+            if (!ready && kb < last) ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
             tc_fence_after();
             tmem_ld16(base + (acc ^ 1u) * 256, r[0]);  // (after the last block: not used)
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), c < 4 ? s0 : s1);
+          for (int e = 0; e < 16; ++e) {
+            if (c == 5 && e == 0) ready = test_wait_fma16(smem_u32(next_full), (acc_i >> 1) & 1u, &sum[c * 16], r[c & 1], s1);
+            if (c != 5) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), c < 4 ? s0 : s1);
+          }
         }
         s0 = x1 * u1;
         s1 = x1 * v1;
