@@ -17,9 +17,11 @@
 // out of tensor memory before it adds the last ones of this block.
 //
 // Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers (even CTA),
-// one for each product, warp 3 the group bounds, warps 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two products.
-// The columns of product h are two runs, one from each CTA's half of the tile:
-// [h w / 4, (h + 1) w / 4) and w / 2 further, w the tile's columns.
+// one for each product, warp 3 the group bounds, warps 4-11 epilogue: warp w reads
+// lanes 32 (w % 4) .. + 31 of one of the two products.  The columns of product h
+// are two runs, one from each CTA's half of the tile: [h w / 4, (h + 1) w / 4) and
+// w / 2 further, w the tile's columns.  Results go through 4 KB of shared memory
+// per warp, so that a store writes 128 bytes of a row and not 16.
 // The tiles of a partial last wave are cut along W into 128- or 64-column pieces.
 #pragma once
 #include "grouped.cuh"
@@ -29,14 +31,15 @@ namespace rmm {
 struct GroupedFp8Cfg {
   static constexpr int X_BYTES = 128 * 128;  // this CTA's 128 rows x 128 contraction indices
   static constexpr int W_BYTES = 128 * 128;  // its 128 of the 256 columns
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 5;
+  static constexpr int OUT_BYTES = 8 * 32 * 128;  // 32 rows x 64 bf16 columns for each epilogue warp
   static constexpr int THREADS = 384;
   // registers per thread at launch, and the split after the set-up: 128 sums and
   // two 32-column loads in flight per epilogue thread (the host checks that the
   // kernel was compiled to LAUNCH_REGS, on which the split draws)
   static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 56, EPI_REGS = 224;
   static_assert(OTHER_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "three warpgroups share what was launched");
-  static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + 256 + (2 * groups + 2) * 4; }
+  static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + OUT_BYTES + 256 + (2 * groups + 2) * 4; }
   static_assert(8 * (2 * STAGES + 9) + 8 <= 256, "barrier area");
 };
 
@@ -116,7 +119,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(grouped_fp8_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sX = smem;
   uint8_t* sW = smem + STAGES * C::X_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sW + STAGES * C::W_BYTES);  // used in the even CTA
+  uint8_t* sOut = sW + STAGES * C::W_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);  // used in the even CTA
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 4;  // used in the even CTA; both [accumulator][half]
@@ -255,34 +259,41 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     set_max_regs_up<C::EPI_REGS>();
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tempty_even = map_shared_rank(smem_u32(&tempty[0]), 0u);
+    const uint32_t base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+    uint8_t* out = sOut + (warp - 4) * 4096;
     uint32_t acc_i = 0;
     bool ok = true;
-    for (int unit = worker; ok && unit < units.count; unit += workers) {
-      const GroupedTile t = units.get(unit);
+    // the tile at hand, where its scales stand for the block after the ones loaded,
+    // and the scales of its first two blocks
+    GroupedTile t;
+    const float *px, *pu, *pv;
+    float x0, u0, v0, x1, u1, v1;
+    auto next_scales = [&](int kb, float& x, float& u, float& v) {  // of block kb; past the last one its own again
+      x = ldg_f32_pinned(px);
+      u = ldg_f32_pinned(pu);
+      v = ldg_f32_pinned(pv);
+      const bool on = kb + 1 < p.num_kb;
+      px += on ? p.lds : 0;
+      pu += on ? p.sw_cols : 0;
+      pv += on ? p.sw_cols : 0;
+    };
+    auto begin = [&](int unit) {
+      t = units.get(unit);
       const int row = t.row0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-      const int run = t.w / 4;                   // columns of each of this thread's two runs
-      const int col0 = t.mtile + half * run;     // the first run's; the second starts t.w / 2 further
-      const bool row_ok = row < t.row_end;
-      const float* sx = p.sx + (row_ok ? row : 0);
+      px = p.sx + (row < t.row_end ? row : 0);
+      // a run of columns lies in one 128-column block of scales (past the edge: any)
       const float* sw = p.sw + static_cast<int64_t>(t.group) * p.num_kb * p.sw_cols;
-      // a run lies in one 128-column block of scales (past the edge: any)
-      const int sb0 = min(col0 / 128, p.sw_cols - 1), sb1 = min((col0 + t.w / 2) / 128, p.sw_cols - 1);
-      const uint32_t base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+      const int col0 = t.mtile + half * (t.w / 4);
+      pu = sw + min(col0 / 128, p.sw_cols - 1);
+      pv = sw + min((col0 + t.w / 2) / 128, p.sw_cols - 1);
+      next_scales(0, x0, u0, v0);
+      next_scales(1, x1, u1, v1);
+    };
+    if (worker < units.count) begin(worker);
+    for (int unit = worker; unit < units.count; unit += workers) {
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
-      // scales of the block being added and of the next two (past the last block: its own again)
-      const int last = p.num_kb - 1;
-      auto load_scales = [&](int kb, float& x, float& u, float& v) {
-        const int64_t b = min(kb, last);
-        x = ldg_f32_pinned(sx + b * p.lds);
-        u = ldg_f32_pinned(sw + sb0 + b * p.sw_cols);
-        v = ldg_f32_pinned(sw + sb1 + b * p.sw_cols);
-      };
-      float x1, u1, v1;
-      load_scales(0, x1, u1, v1);
-      float s0 = x1 * u1, s1 = x1 * v1;
-      load_scales(1, x1, u1, v1);
       uint32_t r[2][16];
       ok = mbar_wait(&tfull[(acc_i & 1u) * 2 + half], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
       if (!ok) break;
@@ -291,8 +302,11 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       for (int kb = 0; ok && kb < p.num_kb; ++kb) {
         const uint32_t acc = acc_i & 1u;
         ++acc_i;
-        float x2, u2, v2;
-        load_scales(kb + 2, x2, u2, v2);
+        const float s0 = x0 * u0, s1 = x0 * v0;
+        x0 = x1;
+        u0 = u1;
+        v0 = v1;
+        next_scales(kb + 2, x1, u1, v1);
         // 16 columns at a time, the next 16 on their way (a narrow piece reads past
         // its columns, inside the accumulator; those sums are not stored).  The
         // loads stand outside every branch, and the additions keep their place:
@@ -308,7 +322,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (elect_one()) mbar_arrive_cluster_relaxed(tempty_even + 8u * (acc * 2 + half));
-            if (!ready && kb < last) ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
+            if (!ready && kb + 1 < p.num_kb)
+              ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
             tc_fence_after();
             tmem_ld16(base + (acc ^ 1u) * 256, r[0]);  // (after the last block: not used)
           }
@@ -318,35 +333,48 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
             if (c != 5) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), c < 4 ? s0 : s1);
           }
         }
-        s0 = x1 * u1;
-        s1 = x1 * v1;
-        x1 = x2;
-        u1 = u2;
-        v1 = v2;
       }
       tmem_ld_wait();
       if (!ok) break;
-      if (row_ok) {
-        uint16_t* y = p.Y + static_cast<int64_t>(row) * p.ldy;
+      const int run = t.w / 4;                // columns of each of this warp's two runs
+      const int col0 = t.mtile + half * run;  // the first run's; the second starts t.w / 2 further
+      const int skip = t.w / 2 - run;
+      const int row0 = t.row0 + static_cast<int>(rank) * 128 + quarter * 32;
+      const int row_end = t.row_end;
+      if (unit + workers < units.count) begin(unit + workers);  // its scales come while this tile is written
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          // accumulator columns 8 c .. 8 c + 7
-          if (c * 8 >= 2 * run) break;
-          const int second = c * 8 >= run ? 1 : 0;
-          const int col = col0 + second * (t.w / 2 - run) + c * 8;
-          const int left = p.m - col;  // columns of this 16-byte piece that exist
+      for (int q = 0; q < 2; ++q) {  // accumulator columns 64 q .. 64 q + 63
+        if (q * 64 >= 2 * run) break;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(sum[c * 8 + 2 * e], sum[c * 8 + 2 * e + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(sum[q * 64 + k * 8 + 2 * e], sum[q * 64 + k * 8 + 2 * e + 1]);
             w[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          if (left >= 8) {
-            *reinterpret_cast<uint4*>(y + col) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
+          *reinterpret_cast<uint4*>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        const int k = lane & 7;              // 8 columns of this thread's rows lane / 8, + 4, ...
+        const int a = q * 64 + k * 8;
+        const int col = col0 + a + (a >= run ? skip : 0);
+        const int left = a < 2 * run ? p.m - col : 0;  // columns that exist
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < left) y[col + e] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
+        for (int it = 0; it < 8; ++it) {
+          const int i = it * 4 + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(out + i * 128 + ((k ^ (i & 7)) << 4));
+          if (row0 + i < row_end && left > 0) {
+            uint16_t* y = p.Y + static_cast<int64_t>(row0 + i) * p.ldy + col;
+            if (left >= 8) {
+              *reinterpret_cast<uint4*>(y) = v;
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (e < left) y[e] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) * 16));
+            }
           }
         }
       }
