@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     // the tile at hand, where its scales stand for the block after the ones loaded,
     // and the scales of its first two blocks
     GroupedTile t;
-    const float *px, *pu, *pv;
+    const float *px = nullptr, *pu = nullptr, *pv = nullptr;
     float x0, u0, v0, x1, u1, v1;
     auto next_scales = [&](int kb, float& x, float& u, float& v) {  // of block kb; past the last one its own again
       x = ldg_f32_pinned(px);

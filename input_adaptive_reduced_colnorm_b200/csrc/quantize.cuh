@@ -4,18 +4,25 @@
 // Activations: blocks of 1 row x 128 columns (quantize_rows_kernel); weights:
 // blocks of 128 x 128 (quantize_blocks_kernel).
 //
-// Bound by memory (2 bytes read, 1 written per element); each element is read
-// once and stays in registers between the maximum and the division.
+// Bound by memory (2 bytes read, 1 written per element) as long as the
+// instructions per element stay near 5: a first version (one IEEE division per
+// scale, scalar arithmetic, 16 lanes per block) was bound by issue slots at 58 %
+// of the copy bandwidth.  Each element is read once and stays in registers between
+// the maximum and the division.
 //
-// The division: with r = fl(1 / s), q0 = fl(x r), the step q = fl(q0 + fl(x - q0 s) r)
-// (Markstein 1990) rounds a number within 2^-47 relative of x / s.  It could
-// only change the e4m3 result where that straddles an fp32 midpoint next to a
-// 5-bit rounding boundary t of e4m3; there x - t s would have to equal half an
-// ulp of t times s up to 2^-47, and as x - t s is a multiple of 2^-4 ulp(s), s
-// would be a short multiple of a power of two and x / s the midpoint itself,
-// which no quotient of fp32 numbers is.  So the codes are those of the IEEE
-// division.  The residual needs x - q0 s above the subnormal range: blocks
-// whose maximum is below 2^-90, zero, infinite or NaN take the division itself.
+// The division, on packed pairs: q0 = x r, q = q0 + (x - q0 s) r with r ~ 1 / s
+// (Markstein 1990) has a relative error below 2^-44 before its last rounding.
+// That gives the codes of the IEEE division: with x and a 8-bit numbers times
+// powers of two, 448 x / a either lies at least 2^-14 (relative) off a rounding
+// boundary t of e4m3 (an odd 5-bit number), far more than all errors here, or is
+// t.  Then s = (a / 448)(1 + e) with e = j / 7 of its last place, j = -3 .. 3, and
+// x / s = t (1 - e) to 2^-46; whether that rounds to t or to a neighbour of t in
+// fp32 turns on (2 j / 7) t / s (mantissas) against 1, and as they differ (equality
+// needs 7 | t, but then a / 448 is exact and e = 0) they do by more than 2^-11.
+// The scale itself is a q0-step on 1 / 448: a / 7 is never nearer to an fp32
+// midpoint than 1 / 14 of the last place.  The residuals need their products above
+// the subnormal range: blocks whose maximum is below 2^-90, infinite or NaN take
+// the division itself.
 #pragma once
 #include <cuda_bf16.h>
 #include "ptx.cuh"
@@ -34,27 +41,22 @@ struct QuantParams {
   int dblocks, mblocks;      // blocks kernel: row and column blocks of one matrix
 };
 
-// |a| and |b| packed, the larger of each half; NaN wins.
+// The larger size of each half, NaN if either is; the sign bits mean nothing.
 __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
-  return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t absmax_words(const uint4& v, uint32_t m) {
-  m = absmax_bf16x2(v.x, m);
-  m = absmax_bf16x2(v.y, m);
-  m = absmax_bf16x2(v.z, m);
-  return absmax_bf16x2(v.w, m);
+  return absmax_bf16x2(absmax_bf16x2(v.x, v.y), absmax_bf16x2(absmax_bf16x2(v.z, v.w), m));
+}
+// of a packed maximum: the larger half
+__device__ __forceinline__ float absmax_value(uint32_t m) {
+  return bf16hi(absmax_bf16x2(m, m << 16) & 0x7FFFFFFFu);
 }
 
-__device__ __forceinline__ float quant_scale(float amax) {
-  const float s = __fdiv_rn(amax, 448.f);
-  return s == 0.f ? 1.f : s;
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
 }
 
 // two values to packed e4m3 (first in the low byte)
@@ -67,20 +69,40 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 struct QuantDiv {
   float s, r;
   bool fast;
-  __device__ __forceinline__ QuantDiv(float amax) : s(quant_scale(amax)) {
-    fast = amax >= 0x1p-90f && amax <= 3.4e38f;  // false for NaN
-    r = fast ? __frcp_rn(s) : 0.f;
-  }
-  __device__ __forceinline__ uint32_t pair(uint32_t w) const {  // two bf16 -> two e4m3
-    const float x0 = bf16lo(w), x1 = bf16hi(w);
+  __device__ __forceinline__ explicit QuantDiv(float amax) {
+    // (zeros, padding as a rule, divide by 1 on the short path; false for NaN)
+    fast = (amax >= 0x1p-90f && amax <= 3.4e38f) || amax == 0.f;
     if (fast) {
-      const float q0 = x0 * r, q1 = x1 * r;
-      return e4m3x2(fmaf(fmaf(-q0, s, x0), r, q0), fmaf(fmaf(-q1, s, x1), r, q1));
+      constexpr float k = 1.f / 448.f;
+      const float q0 = amax * k;
+      s = amax == 0.f ? 1.f : fmaf(fmaf(-q0, 448.f, amax), k, q0);
+      asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    } else {
+      s = __fdiv_rn(amax, 448.f);
+      if (s == 0.f) s = 1.f;
+      r = 0.f;
     }
-    return e4m3x2(__fdiv_rn(x0, s), __fdiv_rn(x1, s));
   }
-  __device__ __forceinline__ uint2 eight(const uint4& v) const {
-    return make_uint2(pair(v.x) | (pair(v.y) << 16), pair(v.z) | (pair(v.w) << 16));
+  // two bf16 -> two e4m3
+  __device__ __forceinline__ uint32_t pair_fast(uint32_t w) const {
+    const uint64_t x = pair_f32(bf16lo(w), bf16hi(w));
+    const uint64_t r2 = pair_f32(r, r), ns2 = pair_f32(-s, -s);
+    uint64_t q0, q;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(x), "l"(r2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(q0), "l"(ns2), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(q), "l"(r2), "l"(q0));
+    return e4m3x2(__uint_as_float(static_cast<uint32_t>(q)), __uint_as_float(static_cast<uint32_t>(q >> 32)));
+  }
+  __device__ __forceinline__ uint32_t pair_div(uint32_t w) const {
+    return e4m3x2(__fdiv_rn(bf16lo(w), s), __fdiv_rn(bf16hi(w), s));
+  }
+  // 16 bf16 -> 16 e4m3
+  __device__ __forceinline__ uint4 sixteen(const uint4& a, const uint4& b) const {
+    if (fast)
+      return make_uint4(pair_fast(a.x) | (pair_fast(a.y) << 16), pair_fast(a.z) | (pair_fast(a.w) << 16),
+                        pair_fast(b.x) | (pair_fast(b.y) << 16), pair_fast(b.z) | (pair_fast(b.w) << 16));
+    return make_uint4(pair_div(a.x) | (pair_div(a.y) << 16), pair_div(a.z) | (pair_div(a.w) << 16),
+                      pair_div(b.x) | (pair_div(b.y) << 16), pair_div(b.z) | (pair_div(b.w) << 16));
   }
 };
 
@@ -93,78 +115,88 @@ __device__ __forceinline__ uint4 quant_load8(const uint16_t* x, int64_t left) {
     if (e < left) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + e)) << ((e & 1) * 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void quant_store8(uint8_t* q, uint2 v, int64_t left) {
-  if (left >= 8) {
-    *reinterpret_cast<uint2*>(q) = v;
+__device__ __forceinline__ void quant_store16(uint8_t* q, const uint4& v, int64_t left) {
+  if (left >= 16) {
+    *reinterpret_cast<uint4*>(q) = v;
     return;
   }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) q[e] = static_cast<uint8_t>((e < 4 ? v.x : v.y) >> ((e & 3) * 8));
+  for (int e = 0; e < 16; ++e)
+    if (e < left) q[e] = static_cast<uint8_t>(w[e >> 2] >> ((e & 3) * 8));
 }
 
-// 16 teams of 16 lanes; a team takes U blocks of one row.  R = 16: the teams
-// take 16 consecutive rows, whose scales are neighbours in memory; R = 1 (fewer
-// than 16 rows): the teams take consecutive blocks of one row.
+// A team of 8 lanes takes a block of one row, 16 columns per lane; a warp four
+// neighbouring blocks (1 KB of the row), U times.  R = 8: the warps of a CTA take
+// 8 consecutive rows, whose scales are neighbours in memory; R = 1 (few rows): they
+// take consecutive blocks of one row.
 template <int R, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
-  const int team = threadIdx.x >> 4, tl = threadIdx.x & 15;
-  constexpr int TB = 16 / R;  // teams side by side along the blocks
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * R + team / TB;
-  const int64_t b0 = static_cast<int64_t>(blockIdx.y) * (TB * U) + team % TB;
+  constexpr int WB = 8 / R;               // warps side by side along the blocks
+  constexpr int CHUNK = WB * 4 * U;       // blocks of one row in a CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tl = lane & 7;
+  const int64_t blocks = (p.d + 127) / 128;
+  const int64_t chunks = (blocks + CHUNK - 1) / CHUNK;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) / chunks * R + warp / WB;
+  const int64_t b0 = static_cast<int64_t>(blockIdx.x) % chunks * CHUNK + (warp % WB) * 4 * U + (lane >> 3);
+  if (row >= p.n) return;
   wait_prior_kernels();
-  uint4 v[U];
+  const uint16_t* x = p.x + row * p.ldx;
+  uint4 v[U][2];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t col = (b0 + u * TB) * 128 + tl * 8;
-    v[u] = (row < p.n && col < p.d) ? quant_load8(p.x + row * p.ldx + col, p.d - col) : make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    uint32_t m = absmax_words(v[u], 0u);
-#pragma unroll
-    for (int k = 8; k >= 1; k /= 2) m = absmax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, k));
-    const QuantDiv dv(max_nan(bf16lo(m), bf16hi(m)));
-    const int64_t blk = b0 + u * TB;
-    const int64_t col = blk * 128 + tl * 8;
-    if (row < p.n && col < p.d) {
-      quant_store8(p.q + row * p.ldq + col, dv.eight(v[u]), p.d - col);
-      if (tl == 0) p.s[blk * p.lds + row] = dv.s;
+    for (int h = 0; h < 2; ++h) {
+      const int64_t col = (b0 + u * 4) * 128 + tl * 16 + h * 8;
+      v[u][h] = col < p.d ? quant_load8(x + col, p.d - col) : make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t m = absmax_words(v[u][1], absmax_words(v[u][0], 0u));
+#pragma unroll
+    for (int k = 4; k >= 1; k /= 2) m = absmax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const QuantDiv dv(absmax_value(m));
+    const int64_t blk = b0 + u * 4;
+    const int64_t col = blk * 128 + tl * 16;
+    if (col < p.d) quant_store16(p.q + row * p.ldq + col, dv.sixteen(v[u][0], v[u][1]), p.d - col);
+    if (tl == 0 && blk < blocks) p.s[blk * p.lds + row] = dv.s;
   }
 }
 
-// One 128 x 128 block per CTA: 16 rows per pass, 16 lanes x 8 columns per row.
+// One 128 x 128 block per CTA: 32 rows per pass, 8 lanes x 16 columns per row.
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const QuantParams p) {
-  __shared__ float warp_max[8];
+  __shared__ uint32_t warp_max[8];
   const int64_t blk = blockIdx.x;
   const int mb = static_cast<int>(blk % p.mblocks);
   const int64_t rest = blk / p.mblocks;
   const int db = static_cast<int>(rest % p.dblocks);
   const int64_t mat = rest / p.dblocks;
-  const int64_t row0 = static_cast<int64_t>(db) * 128 + (threadIdx.x >> 4);
-  const int64_t col = static_cast<int64_t>(mb) * 128 + (threadIdx.x & 15) * 8;
+  const int64_t row0 = static_cast<int64_t>(db) * 128 + (threadIdx.x >> 3);
+  const int64_t col = static_cast<int64_t>(mb) * 128 + (threadIdx.x & 7) * 16;
   const uint16_t* x = p.x + mat * p.xstride + row0 * p.ldx + col;
   uint8_t* q = p.q + mat * p.qstride + row0 * p.ldq + col;
   wait_prior_kernels();
-  uint4 v[8];
+  uint4 v[4][2];
 #pragma unroll
-  for (int u = 0; u < 8; ++u)
-    v[u] = (row0 + u * 16 < p.n && col < p.d) ? quant_load8(x + u * 16 * p.ldx, p.d - col) : make_uint4(0u, 0u, 0u, 0u);
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[u][h] = (row0 + u * 32 < p.n && col + h * 8 < p.d) ? quant_load8(x + u * 32 * p.ldx + h * 8, p.d - col - h * 8)
+                                                           : make_uint4(0u, 0u, 0u, 0u);
   uint32_t m = 0u;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) m = absmax_words(v[u], m);
+  for (int u = 0; u < 4; ++u) m = absmax_words(v[u][1], absmax_words(v[u][0], m));
 #pragma unroll
   for (int k = 16; k >= 1; k /= 2) m = absmax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, k));
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = max_nan(bf16lo(m), bf16hi(m));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
   __syncthreads();
-  float a = warp_max[0];
+  m = warp_max[0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) a = max_nan(a, warp_max[w]);
-  const QuantDiv dv(a);
+  for (int w = 1; w < 8; ++w) m = absmax_bf16x2(m, warp_max[w]);
+  const QuantDiv dv(absmax_value(m));
 #pragma unroll
-  for (int u = 0; u < 8; ++u)
-    if (row0 + u * 16 < p.n && col < p.d) quant_store8(q + u * 16 * p.ldq, dv.eight(v[u]), p.d - col);
+  for (int u = 0; u < 4; ++u)
+    if (row0 + u * 32 < p.n && col < p.d) quant_store16(q + u * 32 * p.ldq, dv.sixteen(v[u][0], v[u][1]), p.d - col);
   if (threadIdx.x == 0) p.s[blk] = dv.s;
 }
 

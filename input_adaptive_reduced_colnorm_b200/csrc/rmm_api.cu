@@ -2088,13 +2088,14 @@ rmm_status rmm_quantize_fp8(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx
   const int64_t blocks = ceil_div(d, 128);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (n < 16)
-    e = launch_chained(quantize_rows_kernel<1, 1>, dim3(static_cast<unsigned>(n), static_cast<unsigned>(ceil_div(blocks, 16))),
-                       dim3(256), 0, s, p);
-  else
-    e = launch_chained(quantize_rows_kernel<16, 4>,
-                       dim3(static_cast<unsigned>(ceil_div(n, 16)), static_cast<unsigned>(ceil_div(blocks, 4))), dim3(256), 0,
-                       s, p);
+  if (n < 64) {
+    const int64_t grid = n * ceil_div(blocks, 32);
+    e = launch_chained(quantize_rows_kernel<1, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+  } else {
+    const int64_t grid = ceil_div(n, 8) * ceil_div(blocks, 8);
+    if (grid > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many blocks");
+    e = launch_chained(quantize_rows_kernel<8, 2>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
   return RMM_OK;
 }
