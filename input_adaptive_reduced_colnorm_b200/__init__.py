@@ -438,36 +438,48 @@ def decode_pv(P, V, rho: float, *, nk=None, out=None, return_idx: bool = False, 
     return (out, idx) if return_idx else out
 
 
-def _current_device(device):
-    """Makes ``device`` current for the library's launches (a no-op where it is)."""
-    import contextlib
+def _matrix(t, name, dtype, dim, device=None):
+    """Checks an operand of the calls below (a matrix or a batch of matrices whose columns are next to one
+    another, on ``device`` if given) and returns its shape and the elements between its rows; for one row, whose
+    stride says nothing, a distance that holds it."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _same_device(first, *others):
-    for t in others:
-        if t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one device")
-
-
-def _rows(t, name):
-    """Elements between the rows of a matrix (or batch of matrices), whose columns must be next to one another; for
-    one row, whose stride says nothing, a distance that holds it."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other operands on {device}")
+    strides = t.stride()
+    cols = shape[-1]
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name} needs unit column stride")
-    return t.stride(-2) if t.shape[-2] > 1 else (t.shape[-1] + 15) // 16 * 16
+    return shape, (strides[-2] if shape[-2] > 1 else (cols + 15) // 16 * 16)
+
+
+def _blocks(x: int) -> int:
+    return (x + 127) // 128
 
 
 def _padded_empty(shape, dtype, device, unit):
-    """An uninitialised tensor whose leading dimension is a multiple of ``unit`` elements."""
+    """An uninitialised tensor whose leading dimension, returned with it, is a multiple of ``unit`` elements."""
     import torch
-    cols = shape[-1]
-    ld = (cols + unit - 1) // unit * unit
-    t = torch.empty((*shape[:-1], ld), dtype=dtype, device=device)
-    return t if ld == cols else t[..., :cols]
+    ld = (shape[-1] + unit - 1) // unit * unit
+    strides = (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device), ld
+
+
+def _run(call, device, *args) -> None:
+    """The C call on ``device`` and its current stream."""
+    import torch
+    index = device.index
+    if torch.cuda.current_device() == index:
+        _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(index):
+            _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 def quantize_fp8(X, *, out=None, scale=None):
@@ -477,22 +489,22 @@ def quantize_fp8(X, *, out=None, scale=None):
     with X ~ Xq * scale: scale = max |x| of the block / 448 (1 where that is 0), Xq = x / scale to nearest even.
     ``out`` needs a row stride that is a multiple of 16 bytes."""
     import torch
-    _require(X, "X", torch.bfloat16, 2)
-    n, d = X.shape
+    (n, d), ldx = _matrix(X, "X", torch.bfloat16, 2)
     dev = X.device
-    blocks = (d + 127) // 128
+    s_shape = (_blocks(d), n)
     if out is None:
-        out = _padded_empty((n, d), torch.float8_e4m3fn, dev, 16)
+        out, ldq = _padded_empty((n, d), torch.float8_e4m3fn, dev, 16)
+    else:
+        shape, ldq = _matrix(out, "out", torch.float8_e4m3fn, 2, dev)
+        if shape != (n, d):
+            raise ValueError(f"out must be {(n, d)}")
     if scale is None:
-        scale = torch.empty((blocks, n), dtype=torch.float32, device=dev)
-    _require(out, "out", torch.float8_e4m3fn, 2)
-    _require(scale, "scale", torch.float32, 2)
-    if out.shape != X.shape or scale.shape != (blocks, n):
-        raise ValueError(f"out must be {tuple(X.shape)} and scale {(blocks, n)}")
-    _same_device(X, out, scale)
-    with _current_device(dev):
-        _check(lib().rmm_quantize_fp8(_ptr(X), n, d, _rows(X, "X"), _ptr(out), _rows(out, "out"), _ptr(scale),
-                                      _rows(scale, "scale"), _stream(dev)))
+        scale, lds = torch.empty(s_shape, dtype=torch.float32, device=dev), n
+    else:
+        shape, lds = _matrix(scale, "scale", torch.float32, 2, dev)
+        if shape != s_shape:
+            raise ValueError(f"scale must be {s_shape}")
+    _run(lib().rmm_quantize_fp8, dev, X.data_ptr(), n, d, ldx, out.data_ptr(), ldq, scale.data_ptr(), lds)
     return out, scale
 
 
@@ -502,69 +514,78 @@ def quantize_fp8_weight(W, *, out=None, scale=None):
     W [d, m] or [groups, d, m] bf16 CUDA -> (Wq of W's shape, float8_e4m3fn, scales [(groups,) ceil(d / 128),
     ceil(m / 128)] float32), as linear_fp8 and grouped_linear_fp8 take them."""
     import torch
-    _require(W, "W", torch.bfloat16)
-    if W.dim() not in (2, 3):
-        raise ValueError("W must be [d, m] or [groups, d, m]")
+    dim = 3 if isinstance(W, torch.Tensor) and W.dim() == 3 else 2
+    shape, ldw = _matrix(W, "W", torch.bfloat16, dim)
     dev = W.device
-    d, m = W.shape[-2:]
-    shape = (*W.shape[:-2], (d + 127) // 128, (m + 127) // 128)
+    d, m = shape[-2:]
+    s_shape = (*shape[:-2], _blocks(d), _blocks(m))
     if out is None:
-        out = _padded_empty(tuple(W.shape), torch.float8_e4m3fn, dev, 16)
+        out, ldq = _padded_empty(tuple(shape), torch.float8_e4m3fn, dev, 16)
+    else:
+        o_shape, ldq = _matrix(out, "out", torch.float8_e4m3fn, dim, dev)
+        if o_shape != shape:
+            raise ValueError(f"out must be {tuple(shape)}")
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=dev)
-    _require(out, "out", torch.float8_e4m3fn, W.dim())
-    _require(scale, "scale", torch.float32, W.dim())
-    if out.shape != W.shape or tuple(scale.shape) != shape or not scale.is_contiguous():
-        raise ValueError(f"out must be {tuple(W.shape)} and scale {shape}, contiguous")
-    _same_device(W, out, scale)
-    groups = W.shape[0] if W.dim() == 3 else 1
-    ws, qs = (W.stride(0), out.stride(0)) if W.dim() == 3 else (0, 0)
-    with _current_device(dev):
-        _check(lib().rmm_quantize_fp8_weight(_ptr(W), groups, ws, d, m, _rows(W, "W"), _ptr(out), qs, _rows(out, "out"),
-                                             _ptr(scale), _stream(dev)))
+        scale = torch.empty(s_shape, dtype=torch.float32, device=dev)
+    else:
+        _matrix(scale, "scale", torch.float32, dim, dev)
+        if scale.shape != s_shape or not scale.is_contiguous():
+            raise ValueError(f"scale must be {s_shape}, contiguous")
+    groups, ws, qs = (shape[0], W.stride(0), out.stride(0)) if dim == 3 else (1, 0, 0)
+    _run(lib().rmm_quantize_fp8_weight, dev, W.data_ptr(), groups, ws, d, m, ldw, out.data_ptr(), qs, ldq, scale.data_ptr())
     return out, scale
+
+
+def _fp8_operands(Xq, x_scale, Wq, w_scale, dim):
+    """Checks the operands of an fp8 product (dim = 3: grouped weights): n, d, m and the leading dimensions."""
+    import torch
+    (n, d), ldx = _matrix(Xq, "Xq", torch.float8_e4m3fn, 2)
+    dev = Xq.device
+    w_shape, ldw = _matrix(Wq, "Wq", torch.float8_e4m3fn, dim, dev)
+    x_scale_shape, lds = _matrix(x_scale, "x_scale", torch.float32, 2, dev)
+    w_scale_shape, _ = _matrix(w_scale, "w_scale", torch.float32, dim, dev)
+    m = w_shape[-1]
+    if w_shape[-2] != d:
+        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {w_shape[-2]} rows")
+    if x_scale_shape != (_blocks(d), n):
+        raise ValueError(f"x_scale must be {(_blocks(d), n)}")
+    if w_scale_shape != (*w_shape[:-2], _blocks(d), _blocks(m)) or not w_scale.is_contiguous():
+        raise ValueError(f"w_scale must be {(*w_shape[:-2], _blocks(d), _blocks(m))}, contiguous")
+    return n, d, m, ldx, lds, ldw
 
 
 def _product_out(out, n, m, device):
     import torch
     if out is None:
         return _padded_empty((n, m), torch.bfloat16, device, 8)
-    _require(out, "out", torch.bfloat16, 2)
-    if out.shape != (n, m):
+    shape, ldy = _matrix(out, "out", torch.bfloat16, 2, device)
+    if shape != (n, m):
         raise ValueError(f"out must be {(n, m)}")
-    return out
+    return out, ldy
 
 
 def linear_fp8(Xq, x_scale, Wq, w_scale, *, out=None):
     """Y = (Xq * x_scale) . (Wq * w_scale) with fp32 sums, for operands as quantize_fp8 and quantize_fp8_weight give
     them: Xq [n, d] and Wq [d, m] float8_e4m3fn (row strides multiples of 16 bytes), x_scale [ceil(d / 128), n],
     w_scale [ceil(d / 128), ceil(m / 128)] float32, CUDA.  Returns Y [n, m] bf16."""
-    import torch
-    _require(Xq, "Xq", torch.float8_e4m3fn, 2)
-    _require(Wq, "Wq", torch.float8_e4m3fn, 2)
-    _require(x_scale, "x_scale", torch.float32, 2)
-    _require(w_scale, "w_scale", torch.float32, 2)
-    n, d = Xq.shape
-    d2, m = Wq.shape
-    if d2 != d:
-        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {d2} rows")
-    blocks = (d + 127) // 128
-    if x_scale.shape != (blocks, n) or w_scale.shape != (blocks, (m + 127) // 128) or not w_scale.is_contiguous():
-        raise ValueError(f"x_scale must be {(blocks, n)} and w_scale {(blocks, (m + 127) // 128)}, contiguous")
+    n, d, m, ldx, lds, ldw = _fp8_operands(Xq, x_scale, Wq, w_scale, 2)
     dev = Xq.device
-    out = _product_out(out, n, m, dev)
-    _same_device(Xq, Wq, x_scale, w_scale, out)
-    with _current_device(dev):
-        _check(lib().rmm_linear_fp8(_ptr(Xq), n, d, _rows(Xq, "Xq"), _ptr(x_scale), _rows(x_scale, "x_scale"), _ptr(Wq),
-                                    m, _rows(Wq, "Wq"), _ptr(w_scale), _ptr(out), _rows(out, "out"), _stream(dev)))
+    out, ldy = _product_out(out, n, m, dev)
+    _run(lib().rmm_linear_fp8, dev, Xq.data_ptr(), n, d, ldx, x_scale.data_ptr(), lds, Wq.data_ptr(), m, ldw,
+         w_scale.data_ptr(), out.data_ptr(), ldy)
     return out
 
 
-def _check_groups(offsets, groups):
+def _check_groups(offsets, groups, device):
     import torch
-    _require(offsets, "offsets", torch.int32, 1)
-    if offsets.numel() != groups + 1 or not offsets.is_contiguous():
+    if not isinstance(offsets, torch.Tensor) or not offsets.is_cuda:
+        raise TypeError("offsets must be a CUDA tensor (the library has no CPU path)")
+    if offsets.dtype is not torch.int32:
+        raise TypeError(f"offsets must be {torch.int32}, got {offsets.dtype}")
+    if offsets.shape != (groups + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets must hold {groups + 1} contiguous entries (one more than the groups)")
+    if offsets.device != device:
+        raise ValueError(f"offsets are on {offsets.device}, other operands on {device}")
 
 
 def grouped_linear(X, W, offsets, *, out=None):
@@ -573,46 +594,28 @@ def grouped_linear(X, W, offsets, *, out=None):
     call does not synchronise; values are clamped to 0 <= ... <= n and to be non-decreasing).  Returns Y [n, m]
     bf16; rows in no group are left as they were (uninitialised without ``out``)."""
     import torch
-    _require(X, "X", torch.bfloat16, 2)
-    _require(W, "W", torch.bfloat16, 3)
-    n, d = X.shape
-    groups, d2, m = W.shape
+    (n, d), ldx = _matrix(X, "X", torch.bfloat16, 2)
+    dev = X.device
+    (groups, d2, m), ldw = _matrix(W, "W", torch.bfloat16, 3, dev)
     if d2 != d:
         raise ValueError(f"contraction mismatch: X has {d} columns, W has {d2} rows")
-    _check_groups(offsets, groups)
-    dev = X.device
-    out = _product_out(out, n, m, dev)
-    _same_device(X, W, offsets, out)
-    with _current_device(dev):
-        _check(lib().rmm_grouped_linear(_ptr(X), n, d, _rows(X, "X"), _ptr(W), groups, W.stride(0), m, _rows(W, "W"),
-                                        _ptr(offsets), _ptr(out), _rows(out, "out"), _stream(dev)))
+    _check_groups(offsets, groups, dev)
+    out, ldy = _product_out(out, n, m, dev)
+    _run(lib().rmm_grouped_linear, dev, X.data_ptr(), n, d, ldx, W.data_ptr(), groups, W.stride(0), m, ldw,
+         offsets.data_ptr(), out.data_ptr(), ldy)
     return out
 
 
 def grouped_linear_fp8(Xq, x_scale, Wq, w_scale, offsets, *, out=None):
     """grouped_linear on e4m3 operands with block scales (see linear_fp8): Xq [n, d], Wq [groups, d, m]
     float8_e4m3fn, x_scale [ceil(d / 128), n], w_scale [groups, ceil(d / 128), ceil(m / 128)] float32."""
-    import torch
-    _require(Xq, "Xq", torch.float8_e4m3fn, 2)
-    _require(Wq, "Wq", torch.float8_e4m3fn, 3)
-    _require(x_scale, "x_scale", torch.float32, 2)
-    _require(w_scale, "w_scale", torch.float32, 3)
-    n, d = Xq.shape
-    groups, d2, m = Wq.shape
-    if d2 != d:
-        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {d2} rows")
-    blocks = (d + 127) // 128
-    w_shape = (groups, blocks, (m + 127) // 128)
-    if x_scale.shape != (blocks, n) or tuple(w_scale.shape) != w_shape or not w_scale.is_contiguous():
-        raise ValueError(f"x_scale must be {(blocks, n)} and w_scale {w_shape}, contiguous")
-    _check_groups(offsets, groups)
+    n, d, m, ldx, lds, ldw = _fp8_operands(Xq, x_scale, Wq, w_scale, 3)
     dev = Xq.device
-    out = _product_out(out, n, m, dev)
-    _same_device(Xq, Wq, x_scale, w_scale, offsets, out)
-    with _current_device(dev):
-        _check(lib().rmm_grouped_linear_fp8(_ptr(Xq), n, d, _rows(Xq, "Xq"), _ptr(x_scale), _rows(x_scale, "x_scale"),
-                                            _ptr(Wq), groups, Wq.stride(0), m, _rows(Wq, "Wq"), _ptr(w_scale),
-                                            _ptr(offsets), _ptr(out), _rows(out, "out"), _stream(dev)))
+    groups = Wq.shape[0]
+    _check_groups(offsets, groups, dev)
+    out, ldy = _product_out(out, n, m, dev)
+    _run(lib().rmm_grouped_linear_fp8, dev, Xq.data_ptr(), n, d, ldx, x_scale.data_ptr(), lds, Wq.data_ptr(), groups,
+         Wq.stride(0), m, ldw, w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), ldy)
     return out
 
 
