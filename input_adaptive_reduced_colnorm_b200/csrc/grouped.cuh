@@ -28,6 +28,11 @@
 // its row count rounded up to 16 (32 for a pair).  When the tiles do not fill a
 // whole number of waves, those of the last wave are cut into narrower ones.
 //
+// Few tiles (decoding): the contraction of a tile is split over the 2 to 8 CTAs of
+// a cluster; they leave their fp32 sums in shared memory and each adds up, in the
+// order of the ranks, some of the columns of all of them (no atomics, no workspace,
+// the same result every time).
+//
 // Group bounds are read on the device (the call does not synchronise): every CTA
 // clamps them to 0 <= ... <= n, non-decreasing, and sums the row tiles of the
 // groups before it starts; a tile number is looked up by bisection.
@@ -51,6 +56,7 @@ struct GroupedParams {
   int n, m;
   int num_kb;              // 128-byte blocks of the contraction
   int m_tiles;             // tiles of CG * MT * 128 columns
+  int splits;              // CTAs of a cluster that share one tile's contraction (CG = 1); 1: none
   uint16_t* Y;
   int64_t ldy;
   // block scales (e4m3)
@@ -60,7 +66,7 @@ struct GroupedParams {
   int sw_cols;
 };
 
-template <int N, int MT, int CG>
+template <int N, int MT, int CG, int OCC>
 struct GroupedCfg {
   static constexpr int A_BYTES = MT * 128 * 128;
   static constexpr int X_ROWS = N / CG;
@@ -69,7 +75,10 @@ struct GroupedCfg {
   static constexpr int HC = COLS / 2;          // columns of one epilogue thread
   static constexpr int TMEM_COLS = 2 * COLS;
   static constexpr int SCALE_BYTES = 8 * 2 * HC * 4;
-  static constexpr int STAGES_FIT = (232448 - 1024 - 256 - SCALE_BYTES - (2 * kGroupedMaxGroups + 2) * 4) / (A_BYTES + X_BYTES);
+  // OCC CTAs share an SM (with the bounds of up to 128 groups; more lower it to one)
+  static constexpr int BOUND_GROUPS = OCC == 1 ? kGroupedMaxGroups : 128;
+  static constexpr int STAGES_FIT =
+      (233472 / OCC - 1024 - 1024 - 256 - SCALE_BYTES - (2 * BOUND_GROUPS + 2) * 4) / (A_BYTES + X_BYTES);
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static_assert(STAGES >= 3, "at least three stages");
   static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory");
@@ -238,11 +247,11 @@ __device__ __forceinline__ void grouped_store(const GroupedParams& p, const uint
   }
 }
 
-template <bool FP8, int N, int MT, int CG>
-__global__ void __launch_bounds__(kGroupedThreads, 1)
+template <bool FP8, int N, int MT, int CG, int OCC>
+__global__ void __launch_bounds__(kGroupedThreads, OCC)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const GroupedParams p) {
-  using C = GroupedCfg<N, MT, CG>;
+  using C = GroupedCfg<N, MT, CG, OCC>;
   constexpr int STAGES = C::STAGES, HC = C::HC;
   constexpr int BK = FP8 ? 128 : 64;
   // the instructions' N is set per tile
@@ -267,7 +276,12 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;  // 0: the CTA that issues the MMAs
-  const int worker = static_cast<int>(blockIdx.x) / CG, workers = static_cast<int>(gridDim.x) / CG;
+  const int splits = CG == 2 ? 1 : p.splits;
+  const uint32_t part = splits > 1 ? cluster_ctarank() : 0u;
+  // with splits every cluster has one tile at most
+  const int worker = static_cast<int>(blockIdx.x) / (CG * splits), workers = static_cast<int>(gridDim.x) / (CG * splits);
+  const int kb_begin = splits > 1 ? static_cast<int>(static_cast<int64_t>(part) * p.num_kb / splits) : 0;
+  const int kb_end = splits > 1 ? static_cast<int>(static_cast<int64_t>(part + 1) * p.num_kb / splits) : p.num_kb;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -313,7 +327,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         if (t.w == 0) continue;
         const int f0 = (t.mtile * CG + static_cast<int>(rank)) * MT * 128;
         const int row = t.row0 + static_cast<int>(rank) * (t.w / 2);  // half of a pair's rows
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer)) {
             ok = false;
             break;
@@ -370,10 +384,10 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const int w = units.get(unit).w;
         if (w == 0) continue;
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w >> 3) << 17);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
           const uint32_t acc = acc_i & 1u;
           bool go = true;
-          if (FP8 || kb == 0)
+          if (FP8 || kb == kb_begin)
             go = mbar_wait(&tempty[acc], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0,
                            CG == 2 ? kMbarClusterRelaxed : kMbarCta);
           go = go && mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma);
@@ -382,14 +396,14 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             break;
           }
           tc_fence_after();
-          const bool last = FP8 || kb == p.num_kb - 1;
+          const bool last = FP8 || kb == kb_end - 1;
           if (elect_one()) {
             const uint32_t d_tmem = tmem_base + acc * C::COLS;
             const uint64_t ad = ad0 + static_cast<uint64_t>(stage * (C::A_BYTES >> 4));
             const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t add = (kk != 0 || (!FP8 && kb != 0)) ? 1u : 0u;
+              const uint32_t add = (kk != 0 || (!FP8 && kb != kb_begin)) ? 1u : 0u;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 const uint64_t am = ad + static_cast<uint64_t>((mt * 16384 + kk * A_STEP) >> 4);
@@ -440,6 +454,9 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HC);
     const uint32_t tempty_even = CG == 2 ? map_shared_rank(smem_u32(&tempty[0]), 0u) : 0u;
     float* my_scale = sScale + (warp - 2) * 2 * HC;
+    // this thread's sums with splits, [HC / 2][32 lanes] per warp, over the stages
+    // (every copy and product of the one tile is complete when they are written)
+    uint64_t* my_part = reinterpret_cast<uint64_t*>(smem) + (warp - 2) * (HC / 2) * 32 + lane;
     uint32_t acc_i = 0;
     bool ok = true;
     auto release = [&](uint32_t acc) {  // this warp has read the accumulator
@@ -463,25 +480,27 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
           for (int j = 0; j < 4; ++j) sum[g][j] = 0;
         // scales of this warp's HC rows (lane, lane + 32, ...) and of the weight
         // blocks, loaded one block ahead
-        float nx[HC / 32], nw[HC / 32];
+        constexpr int SC = (HC + 31) / 32;
+        float nx[SC], nw[SC];
         auto load_scales = [&](int kb) {
 #pragma unroll
-          for (int i = 0; i < HC / 32; ++i) {
+          for (int i = 0; i < SC; ++i) {
             const int row = t.row0 + r_of(i * 32 + lane);
             const int mb = mblock0 + mt_of(i * 32 + lane);
-            const bool there = row < t.row_end && mb < p.sw_cols;
+            const bool there = i * 32 + lane < HC && row < t.row_end && mb < p.sw_cols;
             nx[i] = there ? __ldg(p.sx + kb * p.lds + row) : 0.f;
             nw[i] = there ? __ldg(p.sw + (static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb) : 0.f;
           }
         };
-        load_scales(0);
-        for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
+        load_scales(kb_begin);
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++acc_i) {
           const uint32_t acc = acc_i & 1u;
           float* sc = my_scale + acc * HC;
 #pragma unroll
-          for (int i = 0; i < HC / 32; ++i) sc[i * 32 + lane] = nx[i] * nw[i];
+          for (int i = 0; i < SC; ++i)
+            if (i * 32 + lane < HC) sc[i * 32 + lane] = nx[i] * nw[i];
           __syncwarp();
-          if (kb + 1 < p.num_kb) load_scales(kb + 1);
+          if (kb + 1 < kb_end) load_scales(kb + 1);
           if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) {
             ok = false;
             break;
@@ -509,10 +528,15 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
               }
             }
             if (c + 1 < HC / 16) tmem_ld_wait();
-            if (c + 2 == HC / 16 || HC == 16) release(acc);
+            if (c + 2 == HC / 16 || (HC == 16 && c == 0)) release(acc);
           }
         }
         if (!ok) break;
+        if (splits > 1) {
+#pragma unroll
+          for (int i = 0; i < HC / 2; ++i) my_part[i * 32] = sum[i / 4][i % 4];
+          break;
+        }
 #pragma unroll
         for (int g = 0; g < HC / 8; ++g)
           grouped_store(p, sum[g], t.row0 + r_of(g * 8), t.row_end, (mblock0 + mt_of(g * 8)) * 128 + quarter * 32, lane);
@@ -533,6 +557,11 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             uint64_t v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = pack_u64(r[j >> 1][g * 4 + (j & 1) * 2], r[j >> 1][g * 4 + (j & 1) * 2 + 1]);
+            if (splits > 1) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) my_part[((c * 2 + g) * 4 + j) * 32] = v[j];
+              continue;
+            }
             grouped_store(p, v, t.row0 + r_of(c * 16 + g * 8), t.row_end,
                           (mblock0 + mt_of(c * 16 + g * 8)) * 128 + quarter * 32, lane);
           }
@@ -542,8 +571,39 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     }
   }
 
+  if (CG == 1 && splits > 1) {
+    cluster_sync();  // every CTA's sums are there
+    if (warp >= 2 && worker < units.count) {
+      const GroupedTile t = units.get(worker);
+      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((((warp - 2) * (HC / 2)) * 32 + lane) * 8);
+#pragma unroll
+      for (int g = 0; g < HC / 8; ++g) {
+        if (g % splits != static_cast<int>(part)) continue;
+        float2 s[4] = {};
+        for (int r = 0; r < splits; ++r) {
+          const uint32_t from = map_shared_rank(at, static_cast<uint32_t>(r));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = ld_shared_cluster_f32x2(from + static_cast<uint32_t>((g * 4 + j) * 32 * 8));
+            s[j].x += v.x;
+            s[j].y += v.y;
+          }
+        }
+        uint64_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = pack_u64(__float_as_uint(s[j].x), __float_as_uint(s[j].y));
+        const int i = g * 8;
+        const int mt = HC >= N ? half * (HC / N) + i / N : 0;
+        const int row = HC >= N ? i % N : half * HC + i;
+        grouped_store(p, v, t.row0 + row, t.row_end, (t.mtile * MT + mt) * 128 + quarter * 32, lane);
+      }
+    }
+  }
   tc_fence_before();
-  if (CG == 2) cluster_sync();  // both CTAs are done with every MMA, copy and accumulator
+  // both CTAs of a pair are done with every MMA, copy and accumulator, the CTAs of
+  // a split tile with one another's sums
+  if (CG == 2 || splits > 1) cluster_sync();
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();

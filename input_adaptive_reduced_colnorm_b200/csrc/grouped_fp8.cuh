@@ -219,18 +219,20 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
         const uint32_t idesc = make_idesc_e4m3(256, 0, 0, 1) | (static_cast<uint32_t>(w >> 4) << 17);  // N = w / 2
         for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
           const uint32_t buf = (acc_i & 1u) * 2 + h;
+          const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
+          // w / 4 columns of each CTA
+          const uint64_t wd = wd0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4)) + static_cast<uint64_t>((h * (w >> 2)) >> 4);
+          // (the operands are there long before the accumulator: asked first, off the
+          // path from one block's epilogue to the next but one's product)
           const bool go =
-              mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed) &&
-              mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma);
+              mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma) &&
+              mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed);
           if (!__all_sync(0xffffffffu, go)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
-            // w / 4 columns of each CTA
-            const uint64_t wd = wd0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4)) + static_cast<uint64_t>((h * (w >> 2)) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_e4m3_pair(tmem_base + buf * 128, xd + static_cast<uint64_t>(kk * (32 >> 4)),
@@ -263,19 +265,21 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     uint8_t* out = sOut + (warp - 4) * 4096;
     uint32_t acc_i = 0;
     bool ok = true;
-    // the tile at hand, where its scales stand for the block after the ones loaded,
-    // and the scales of its first two blocks
+    // the tile at hand; the row's scales of the next two blocks and where the one
+    // after stands; the weight blocks' scales of 32 blocks, one per lane (uniform
+    // over the warp, they are passed on by shuffles: two loads a block less)
     GroupedTile t;
     const float *px = nullptr, *pu = nullptr, *pv = nullptr;
-    float x0, u0, v0, x1, u1, v1;
-    auto next_scales = [&](int kb, float& x, float& u, float& v) {  // of block kb; past the last one its own again
-      x = ldg_f32_pinned(px);
-      u = ldg_f32_pinned(pu);
-      v = ldg_f32_pinned(pv);
-      const bool on = kb + 1 < p.num_kb;
-      px += on ? p.lds : 0;
-      pu += on ? p.sw_cols : 0;
-      pv += on ? p.sw_cols : 0;
+    float x0, x1, u32, v32;
+    auto next_x = [&](int kb) {  // of block kb; past the last one its own again
+      const float x = ldg_f32_pinned(px);
+      px += kb + 1 < p.num_kb ? p.lds : 0;
+      return x;
+    };
+    auto load_w = [&](int kb) {  // of blocks kb .. kb + 31
+      const int64_t at = static_cast<int64_t>(min(kb + lane, p.num_kb - 1)) * p.sw_cols;
+      u32 = ldg_f32_pinned(pu + at);
+      v32 = ldg_f32_pinned(pv + at);
     };
     auto begin = [&](int unit) {
       t = units.get(unit);
@@ -286,8 +290,9 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       const int col0 = t.mtile + half * (t.w / 4);
       pu = sw + min(col0 / 128, p.sw_cols - 1);
       pv = sw + min((col0 + t.w / 2) / 128, p.sw_cols - 1);
-      next_scales(0, x0, u0, v0);
-      next_scales(1, x1, u1, v1);
+      x0 = next_x(0);
+      x1 = next_x(1);
+      load_w(0);
     };
     if (worker < units.count) begin(worker);
     for (int unit = worker; unit < units.count; unit += workers) {
@@ -302,11 +307,10 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       for (int kb = 0; ok && kb < p.num_kb; ++kb) {
         const uint32_t acc = acc_i & 1u;
         ++acc_i;
-        const float s0 = x0 * u0, s1 = x0 * v0;
+        const float s0 = x0 * __shfl_sync(0xffffffffu, u32, kb & 31), s1 = x0 * __shfl_sync(0xffffffffu, v32, kb & 31);
         x0 = x1;
-        u0 = u1;
-        v0 = v1;
-        next_scales(kb + 2, x1, u1, v1);
+        x1 = next_x(kb + 2);
+        if ((kb & 31) == 31) load_w(kb + 1);
         // 16 columns at a time, the next 16 on their way (a narrow piece reads past
         // its columns, inside the accumulator; those sums are not stored).  The
         // loads stand outside every branch, and the additions keep their place:

@@ -1940,9 +1940,15 @@ struct GroupedCall {
   GroupedParams p;
 };
 
-template <bool FP8, int N, int MT, int CG>
+// Tiles of `rows` rows x `cols` columns that a call is taken to have: its groups as
+// even as they can be, one tile at least for each (the bounds are on the device).
+int64_t grouped_tiles(const GroupedCall& c, int64_t rows, int64_t cols) {
+  return std::max(ceil_div(c.n, rows), std::min(c.groups, c.n)) * ceil_div(c.m, cols);
+}
+
+template <bool FP8, int N, int MT, int CG, int OCC = 1>
 rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
-  using Cfg = GroupedCfg<N, MT, CG>;
+  using Cfg = GroupedCfg<N, MT, CG, OCC>;
   CUtensorMap tw, tx;
   if (rmm_status st = make_tmaps_grouped(&tw, &tx, FP8, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx,
                                          Cfg::X_ROWS))
@@ -1954,13 +1960,25 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   const int64_t row_tiles = ceil_div(c.n, N) + std::min<int64_t>(c.groups - 1, c.n);
   // (a tile of the last wave may be cut into up to eight)
   if (8 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
-  const int64_t workers = std::min<int64_t>((N >= 128 ? N / 32 : 1) * row_tiles * p.m_tiles, std::max(1, num_sms() / CG));
+  // Few tiles: split each one's contraction over a cluster of 2 or 4 so that about
+  // every SM has a part (clusters of 4 reached 132 of 148 SMs; clusters of 8 only
+  // 120, and at n = 1, 4096 x 4096 e4m3 they took 9.0 us, those of 4 7.6 us, no
+  // split 13.6 us).  A launch has a cluster for every tile that there may be.
+  int64_t splits = 1;
+  if (CG == 1) {
+    const int64_t tiles = grouped_tiles(c, N, MT * 128);
+    if (2 * tiles <= num_sms() * OCC && p.num_kb >= 2) splits = 2;
+    if (4 * tiles <= (num_sms() - 16) * OCC && p.num_kb >= 4) splits = 4;
+  }
+  p.splits = static_cast<int>(splits);
+  const int64_t workers = splits > 1 ? row_tiles * p.m_tiles : std::min<int64_t>((N >= 128 ? N / 32 : 1) * row_tiles * p.m_tiles, std::max(1, num_sms() * OCC / CG));
   const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
-  auto kern = grouped_kernel<FP8, N, MT, CG>;
+  auto kern = grouped_kernel<FP8, N, MT, CG, OCC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
-  const dim3 grid(static_cast<unsigned>(workers * CG));
-  if (CG == 2) e = launch_cluster(kern, grid, dim3(kGroupedThreads), smem, 2, s, tw, tx, p);
+  const dim3 grid(static_cast<unsigned>(workers * CG * splits));
+  if (CG == 2 || splits > 1)
+    e = launch_cluster(kern, grid, dim3(kGroupedThreads), smem, static_cast<int>(CG * splits), s, tw, tx, p);
   else e = launch_chained(kern, grid, dim3(kGroupedThreads), smem, s, tw, tx, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return RMM_OK;
@@ -1993,15 +2011,30 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   return RMM_OK;
 }
 
+// Tile shape by the rows of an average group and the tiles there are (times in us;
+// bf16 unless e4m3 is said):
+//   32 rows x 128 columns where such tiles fit one wave, whatever the rows: a CTA
+//     streams some 75 GB/s, so they have to be many.  n = 1, 4096 x 4096: 9.7
+//     against 11.8 with 512 columns a tile; e4m3 333 x 1000 x 1522: 5.2 against 8.9.
+//     Not where an e4m3 tile would have more than 16 blocks to itself: each costs its
+//     epilogue 0.45 us (1 x 4096 x 14336: 17.3 against 14.9).
+//   16 x 256, two CTAs per SM, up to 16 rows: e4m3 256 x 2048 x 1536 of 128 groups
+//     57 against 59 with 16 x 512 and one CTA.
+//   32 x 512 up to 32 rows: e4m3 256 x 4096 x 14336 of 8 81 against 85 with 16 rows.
+//   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
+//     83 with 32; e4m3 up to 128 rows: 128 x 4096 x 14336 22 against 23 with 256 rows.
+//   256 x 256 on CTA pairs for more, unless their tiles leave most SMs idle (256 x
+//     4096 x 4096: 24 against 20 with 64 rows; 512 x 4096 x 4096: 25 against 28).
 template <bool FP8>
 rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   const int64_t rows = ceil_div(c.n, c.groups);  // of an average group
-  if (rows <= 16) return launch_grouped_t<FP8, 16, 4, 1>(c, s);
+  const int64_t small = grouped_tiles(c, 32, 128);
+  if (small <= num_sms() && (!FP8 || 2 * small <= num_sms() || c.d <= 2048)) return launch_grouped_t<FP8, 32, 1, 1>(c, s);
+  if (rows <= 16) return launch_grouped_t<FP8, 16, 2, 1, 2>(c, s);
   if (rows <= 32) return launch_grouped_t<FP8, 32, 4, 1>(c, s);
-  if (rows <= 64) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
-  if (rows <= 128) return launch_grouped_t<FP8, 128, 2, 1>(c, s);
-  if (FP8) return launch_grouped_fp8_rows(c, s);
-  return launch_grouped_t<false, 256, 1, 2>(c, s);
+  if (rows <= (FP8 ? 128 : 64) || 5 * grouped_tiles(c, 256, 256) < num_sms()) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
+  if constexpr (FP8) return launch_grouped_fp8_rows(c, s);
+  else return launch_grouped_t<false, 256, 1, 2>(c, s);
 }
 
 // Checks shared by the product calls; `unit` = elements of 16 bytes.
