@@ -438,48 +438,64 @@ def decode_pv(P, V, rho: float, *, nk=None, out=None, return_idx: bool = False, 
     return (out, idx) if return_idx else out
 
 
-def _matrix(t, name, dtype, dim, device=None):
-    """Checks an operand of the calls below (a matrix or a batch of matrices whose columns are next to one
-    another, on ``device`` if given) and returns its shape and the elements between its rows; for one row, whose
-    stride says nothing, a distance that holds it."""
+# The checks of the calls below are written for little host time (a small product takes
+# 5 us of the GPU's): one pass over each operand, the current stream and device as numbers.
+def _refuse(t, name, dtype, dim, index):
+    """Why an operand is refused (see _matrix)."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != dim:
+    if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other operands on {device}")
-    strides = t.stride()
-    cols = shape[-1]
-    if cols > 1 and strides[-1] != 1:
-        raise ValueError(f"{name} needs unit column stride")
-    return shape, (strides[-2] if shape[-2] > 1 else (cols + 15) // 16 * 16)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, other operands on cuda:{index}")
+    raise ValueError(f"{name} needs unit column stride")
 
 
-def _blocks(x: int) -> int:
-    return (x + 127) // 128
-
-
-def _padded_empty(shape, dtype, device, unit):
-    """An uninitialised tensor whose leading dimension, returned with it, is a multiple of ``unit`` elements."""
+def _device_of(t, name) -> int:
     import torch
-    ld = (shape[-1] + unit - 1) // unit * unit
-    strides = (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1)
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device), ld
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    return t.get_device()
 
 
-def _run(call, device, *args) -> None:
-    """The C call on ``device`` and its current stream."""
-    import torch
-    index = device.index
-    if torch.cuda.current_device() == index:
-        _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+def _matrix(t, name, dtype, dim, index):
+    """Checks an operand, a matrix or a batch of matrices whose columns are next to one another, on device ``index``;
+    its shape and the elements between its rows (for one row, whose stride says nothing, a distance that holds it)."""
+    try:
+        shape, strides = t.shape, t.stride()
+        if t.dtype is not dtype or len(shape) != dim or t.get_device() != index or (strides[-1] != 1 and shape[-1] > 1):
+            _refuse(t, name, dtype, dim, index)
+    except AttributeError:
+        _refuse(t, name, dtype, dim, index)
+    return shape, strides[-2] if shape[-2] > 1 else (shape[-1] + 15) // 16 * 16
+
+
+def _contiguous(t, name, dtype, shape, index):
+    """Checks a contiguous operand of exactly ``shape``."""
+    if getattr(t, "dtype", None) is not dtype or len(t.shape) != len(shape) or t.get_device() != index:
+        _refuse(t, name, dtype, len(shape), index)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be {shape}, contiguous")
+
+
+def _rows_empty(torch, n, m, dtype, index, unit):
+    """An uninitialised matrix whose leading dimension, returned with it, is a multiple of ``unit`` elements."""
+    ld = (m + unit - 1) // unit * unit
+    return torch.empty_strided((n, m), (ld, 1), dtype=dtype, device=index), ld
+
+
+def _run(torch, call, index, *args) -> None:
+    """The C call on device ``index`` and its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            _check(call(*args, torch._C._cuda_getCurrentRawStream(index)))
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _check(status)
 
 
 def quantize_fp8(X, *, out=None, scale=None):
@@ -489,22 +505,22 @@ def quantize_fp8(X, *, out=None, scale=None):
     with X ~ Xq * scale: scale = max |x| of the block / 448 (1 where that is 0), Xq = x / scale to nearest even.
     ``out`` needs a row stride that is a multiple of 16 bytes."""
     import torch
-    (n, d), ldx = _matrix(X, "X", torch.bfloat16, 2)
-    dev = X.device
-    s_shape = (_blocks(d), n)
+    index = _device_of(X, "X")
+    (n, d), ldx = _matrix(X, "X", torch.bfloat16, 2, index)
+    blocks = (d + 127) // 128
     if out is None:
-        out, ldq = _padded_empty((n, d), torch.float8_e4m3fn, dev, 16)
+        out, ldq = _rows_empty(torch, n, d, torch.float8_e4m3fn, index, 16)
     else:
-        shape, ldq = _matrix(out, "out", torch.float8_e4m3fn, 2, dev)
+        shape, ldq = _matrix(out, "out", torch.float8_e4m3fn, 2, index)
         if shape != (n, d):
             raise ValueError(f"out must be {(n, d)}")
     if scale is None:
-        scale, lds = torch.empty(s_shape, dtype=torch.float32, device=dev), n
+        scale, lds = torch.empty_strided((blocks, n), (n, 1), dtype=torch.float32, device=index), n
     else:
-        shape, lds = _matrix(scale, "scale", torch.float32, 2, dev)
-        if shape != s_shape:
-            raise ValueError(f"scale must be {s_shape}")
-    _run(lib().rmm_quantize_fp8, dev, X.data_ptr(), n, d, ldx, out.data_ptr(), ldq, scale.data_ptr(), lds)
+        shape, lds = _matrix(scale, "scale", torch.float32, 2, index)
+        if shape != (blocks, n):
+            raise ValueError(f"scale must be {(blocks, n)}")
+    _run(torch, lib().rmm_quantize_fp8, index, X.data_ptr(), n, d, ldx, out.data_ptr(), ldq, scale.data_ptr(), lds)
     return out, scale
 
 
@@ -514,78 +530,64 @@ def quantize_fp8_weight(W, *, out=None, scale=None):
     W [d, m] or [groups, d, m] bf16 CUDA -> (Wq of W's shape, float8_e4m3fn, scales [(groups,) ceil(d / 128),
     ceil(m / 128)] float32), as linear_fp8 and grouped_linear_fp8 take them."""
     import torch
-    dim = 3 if isinstance(W, torch.Tensor) and W.dim() == 3 else 2
-    shape, ldw = _matrix(W, "W", torch.bfloat16, dim)
-    dev = W.device
+    index = _device_of(W, "W")
+    dim = 3 if W.dim() == 3 else 2
+    shape, ldw = _matrix(W, "W", torch.bfloat16, dim, index)
     d, m = shape[-2:]
-    s_shape = (*shape[:-2], _blocks(d), _blocks(m))
+    s_shape = (*shape[:-2], (d + 127) // 128, (m + 127) // 128)
     if out is None:
-        out, ldq = _padded_empty(tuple(shape), torch.float8_e4m3fn, dev, 16)
+        ldq = (m + 15) // 16 * 16
+        strides = (ldq, 1) if dim == 2 else (d * ldq, ldq, 1)
+        out = torch.empty_strided(shape, strides, dtype=torch.float8_e4m3fn, device=index)
     else:
-        o_shape, ldq = _matrix(out, "out", torch.float8_e4m3fn, dim, dev)
+        o_shape, ldq = _matrix(out, "out", torch.float8_e4m3fn, dim, index)
         if o_shape != shape:
             raise ValueError(f"out must be {tuple(shape)}")
     if scale is None:
-        scale = torch.empty(s_shape, dtype=torch.float32, device=dev)
+        scale = torch.empty(s_shape, dtype=torch.float32, device=index)
     else:
-        _matrix(scale, "scale", torch.float32, dim, dev)
-        if scale.shape != s_shape or not scale.is_contiguous():
-            raise ValueError(f"scale must be {s_shape}, contiguous")
+        _contiguous(scale, "scale", torch.float32, s_shape, index)
     groups, ws, qs = (shape[0], W.stride(0), out.stride(0)) if dim == 3 else (1, 0, 0)
-    _run(lib().rmm_quantize_fp8_weight, dev, W.data_ptr(), groups, ws, d, m, ldw, out.data_ptr(), qs, ldq, scale.data_ptr())
+    _run(torch, lib().rmm_quantize_fp8_weight, index, W.data_ptr(), groups, ws, d, m, ldw, out.data_ptr(), qs, ldq,
+         scale.data_ptr())
     return out, scale
 
 
-def _fp8_operands(Xq, x_scale, Wq, w_scale, dim):
-    """Checks the operands of an fp8 product (dim = 3: grouped weights): n, d, m and the leading dimensions."""
-    import torch
-    (n, d), ldx = _matrix(Xq, "Xq", torch.float8_e4m3fn, 2)
-    dev = Xq.device
-    w_shape, ldw = _matrix(Wq, "Wq", torch.float8_e4m3fn, dim, dev)
-    x_scale_shape, lds = _matrix(x_scale, "x_scale", torch.float32, 2, dev)
-    w_scale_shape, _ = _matrix(w_scale, "w_scale", torch.float32, dim, dev)
-    m = w_shape[-1]
-    if w_shape[-2] != d:
-        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {w_shape[-2]} rows")
-    if x_scale_shape != (_blocks(d), n):
-        raise ValueError(f"x_scale must be {(_blocks(d), n)}")
-    if w_scale_shape != (*w_shape[:-2], _blocks(d), _blocks(m)) or not w_scale.is_contiguous():
-        raise ValueError(f"w_scale must be {(*w_shape[:-2], _blocks(d), _blocks(m))}, contiguous")
-    return n, d, m, ldx, lds, ldw
-
-
-def _product_out(out, n, m, device):
-    import torch
+def _product_out(torch, out, n, m, index):
     if out is None:
-        return _padded_empty((n, m), torch.bfloat16, device, 8)
-    shape, ldy = _matrix(out, "out", torch.bfloat16, 2, device)
+        return _rows_empty(torch, n, m, torch.bfloat16, index, 8)
+    shape, ldy = _matrix(out, "out", torch.bfloat16, 2, index)
     if shape != (n, m):
         raise ValueError(f"out must be {(n, m)}")
     return out, ldy
+
+
+def _check_offsets(torch, offsets, groups, index):
+    if getattr(offsets, "dtype", None) is not torch.int32 or offsets.dim() != 1 or offsets.get_device() != index:
+        _refuse(offsets, "offsets", torch.int32, 1, index)
+    if offsets.shape[0] != groups + 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets must hold {groups + 1} contiguous entries (one more than the groups)")
 
 
 def linear_fp8(Xq, x_scale, Wq, w_scale, *, out=None):
     """Y = (Xq * x_scale) . (Wq * w_scale) with fp32 sums, for operands as quantize_fp8 and quantize_fp8_weight give
     them: Xq [n, d] and Wq [d, m] float8_e4m3fn (row strides multiples of 16 bytes), x_scale [ceil(d / 128), n],
     w_scale [ceil(d / 128), ceil(m / 128)] float32, CUDA.  Returns Y [n, m] bf16."""
-    n, d, m, ldx, lds, ldw = _fp8_operands(Xq, x_scale, Wq, w_scale, 2)
-    dev = Xq.device
-    out, ldy = _product_out(out, n, m, dev)
-    _run(lib().rmm_linear_fp8, dev, Xq.data_ptr(), n, d, ldx, x_scale.data_ptr(), lds, Wq.data_ptr(), m, ldw,
+    import torch
+    index = _device_of(Xq, "Xq")
+    (n, d), ldx = _matrix(Xq, "Xq", torch.float8_e4m3fn, 2, index)
+    (d2, m), ldw = _matrix(Wq, "Wq", torch.float8_e4m3fn, 2, index)
+    s_shape, lds = _matrix(x_scale, "x_scale", torch.float32, 2, index)
+    if d2 != d:
+        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {d2} rows")
+    blocks = (d + 127) // 128
+    if s_shape != (blocks, n):
+        raise ValueError(f"x_scale must be {(blocks, n)}")
+    _contiguous(w_scale, "w_scale", torch.float32, (blocks, (m + 127) // 128), index)
+    out, ldy = _product_out(torch, out, n, m, index)
+    _run(torch, lib().rmm_linear_fp8, index, Xq.data_ptr(), n, d, ldx, x_scale.data_ptr(), lds, Wq.data_ptr(), m, ldw,
          w_scale.data_ptr(), out.data_ptr(), ldy)
     return out
-
-
-def _check_groups(offsets, groups, device):
-    import torch
-    if not isinstance(offsets, torch.Tensor) or not offsets.is_cuda:
-        raise TypeError("offsets must be a CUDA tensor (the library has no CPU path)")
-    if offsets.dtype is not torch.int32:
-        raise TypeError(f"offsets must be {torch.int32}, got {offsets.dtype}")
-    if offsets.shape != (groups + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must hold {groups + 1} contiguous entries (one more than the groups)")
-    if offsets.device != device:
-        raise ValueError(f"offsets are on {offsets.device}, other operands on {device}")
 
 
 def grouped_linear(X, W, offsets, *, out=None):
@@ -594,14 +596,14 @@ def grouped_linear(X, W, offsets, *, out=None):
     call does not synchronise; values are clamped to 0 <= ... <= n and to be non-decreasing).  Returns Y [n, m]
     bf16; rows in no group are left as they were (uninitialised without ``out``)."""
     import torch
-    (n, d), ldx = _matrix(X, "X", torch.bfloat16, 2)
-    dev = X.device
-    (groups, d2, m), ldw = _matrix(W, "W", torch.bfloat16, 3, dev)
+    index = _device_of(X, "X")
+    (n, d), ldx = _matrix(X, "X", torch.bfloat16, 2, index)
+    (groups, d2, m), ldw = _matrix(W, "W", torch.bfloat16, 3, index)
     if d2 != d:
         raise ValueError(f"contraction mismatch: X has {d} columns, W has {d2} rows")
-    _check_groups(offsets, groups, dev)
-    out, ldy = _product_out(out, n, m, dev)
-    _run(lib().rmm_grouped_linear, dev, X.data_ptr(), n, d, ldx, W.data_ptr(), groups, W.stride(0), m, ldw,
+    _check_offsets(torch, offsets, groups, index)
+    out, ldy = _product_out(torch, out, n, m, index)
+    _run(torch, lib().rmm_grouped_linear, index, X.data_ptr(), n, d, ldx, W.data_ptr(), groups, W.stride(0), m, ldw,
          offsets.data_ptr(), out.data_ptr(), ldy)
     return out
 
@@ -609,13 +611,21 @@ def grouped_linear(X, W, offsets, *, out=None):
 def grouped_linear_fp8(Xq, x_scale, Wq, w_scale, offsets, *, out=None):
     """grouped_linear on e4m3 operands with block scales (see linear_fp8): Xq [n, d], Wq [groups, d, m]
     float8_e4m3fn, x_scale [ceil(d / 128), n], w_scale [groups, ceil(d / 128), ceil(m / 128)] float32."""
-    n, d, m, ldx, lds, ldw = _fp8_operands(Xq, x_scale, Wq, w_scale, 3)
-    dev = Xq.device
-    groups = Wq.shape[0]
-    _check_groups(offsets, groups, dev)
-    out, ldy = _product_out(out, n, m, dev)
-    _run(lib().rmm_grouped_linear_fp8, dev, Xq.data_ptr(), n, d, ldx, x_scale.data_ptr(), lds, Wq.data_ptr(), groups,
-         Wq.stride(0), m, ldw, w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), ldy)
+    import torch
+    index = _device_of(Xq, "Xq")
+    (n, d), ldx = _matrix(Xq, "Xq", torch.float8_e4m3fn, 2, index)
+    (groups, d2, m), ldw = _matrix(Wq, "Wq", torch.float8_e4m3fn, 3, index)
+    s_shape, lds = _matrix(x_scale, "x_scale", torch.float32, 2, index)
+    if d2 != d:
+        raise ValueError(f"contraction mismatch: Xq has {d} columns, Wq has {d2} rows")
+    blocks = (d + 127) // 128
+    if s_shape != (blocks, n):
+        raise ValueError(f"x_scale must be {(blocks, n)}")
+    _contiguous(w_scale, "w_scale", torch.float32, (groups, blocks, (m + 127) // 128), index)
+    _check_offsets(torch, offsets, groups, index)
+    out, ldy = _product_out(torch, out, n, m, index)
+    _run(torch, lib().rmm_grouped_linear_fp8, index, Xq.data_ptr(), n, d, ldx, x_scale.data_ptr(), lds, Wq.data_ptr(),
+         groups, Wq.stride(0), m, ldw, w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), ldy)
     return out
 
 

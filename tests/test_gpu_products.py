@@ -93,6 +93,7 @@ def test_quantize_every_value_under_many_scales():
         for k in range(0, 20):  # values of every mantissa, down to 2^-19 of the maximum's size
             rows.append(mant[None, :127] * 2.0 ** (e - k) * np.where(np.arange(127) % 2, -1.0, 1.0))
         vals = np.concatenate(rows)                                     # [20, 127]
+        vals[::7, 5] = mant[127] * 2.0 ** (e - 3)
         X = np.concatenate([np.repeat(vals, len(top), 0), np.tile(top, len(vals))[:, None]], 1)
         X = np.minimum(np.abs(X), X[:, -1:]) * np.sign(X)
         Xb = synthetic.to_bf16(X)
@@ -202,6 +203,113 @@ def test_grouped_linear_fp8(sizes, d, m):
     check(Y, ref, mag, d, f"grouped fp8 {sizes} {d} x {m}")
 
 
+# (rows of the groups, d, m): the shapes of tile that the library chooses by the rows of
+# an average group and the number of tiles, each with groups that end inside a tile
+TILES = [
+    ([3, 0, 16, 1, 17, 9], 300, 4200),                     # 16 rows x 256 columns
+    ([30, 1, 33, 32, 0, 16, 40, 31], 200, 2600),           # 32 x 512
+    ([64, 70, 0, 1, 63, 40, 65, 64, 50, 60], 264, 2100),   # 64 x 256
+    ([129, 255, 0, 256, 257, 300, 1], 130, 2300),          # 256 x 256, one wave
+    ([1000, 31, 130], 200, 4100),                          # 256 x 256, a last wave of narrow pieces
+    ([1030], 72, 5000),
+    ([200, 513, 290], 1000, 5100),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("sizes,d,m", TILES, ids=str)
+def test_every_tile_shape(sizes, d, m, fp8):
+    n, E = sum(sizes) + 3, len(sizes)
+    off = bounds_of(sizes, 1)
+    out = padded(torch.full((n, m), 3.0, dtype=torch.bfloat16), 8)
+    if fp8:
+        dev, X, W = fp8_operands(71, n, d, m, E)
+        Y = rmm.grouped_linear_fp8(dev["xq"], dev["sx"], dev["wq"], dev["sw"], off.cuda(), out=out)
+    else:
+        g = synthetic.rng(71)
+        Xb = synthetic.to_bf16(synthetic.outlier_activations(g, n, d, 1.0))
+        Wb = synthetic.to_bf16(g.standard_normal((E, d, m)) / np.sqrt(d))
+        X, W = synthetic.widen(Xb), synthetic.widen(Wb)
+        Y = rmm.grouped_linear(padded(Xb, 8, extra=1), padded(Wb, 8), off.cuda(), out=out)
+    again = Y.clone()
+    ref = oracle.grouped_product(X, W, off.numpy(), np.full((n, m), 3.0))
+    mag = oracle.grouped_product(np.abs(X), [np.abs(w) for w in W], off.numpy(), np.zeros((n, m)))
+    check(Y, ref, mag, d, f"{sizes} {d} x {m}")
+    for _ in range(3):  # the same result every time
+        if fp8:
+            rmm.grouped_linear_fp8(dev["xq"], dev["sx"], dev["wq"], dev["sw"], off.cuda(), out=out)
+        else:
+            rmm.grouped_linear(padded(Xb, 8, extra=1), padded(Wb, 8), off.cuda(), out=out)
+        assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("n,d,m", [(1, 4096, 1000), (20, 2000, 1522), (7, 130, 9000), (40, 8192, 300), (300, 3000, 520)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_split_contraction(n, d, m, fp8):
+    """Few tiles: the contraction of one is shared by a cluster, with block counts that do
+    not divide by its size and row tiles that are not full."""
+    if fp8:
+        dev, X, W = fp8_operands(72, n, d, m)
+        Y = rmm.linear_fp8(dev["xq"], dev["sx"], dev["wq"], dev["sw"])
+        W = W[0]
+    else:
+        g = synthetic.rng(72)
+        Xb = synthetic.to_bf16(synthetic.outlier_activations(g, n, d, 1.0))
+        Wb = synthetic.to_bf16(g.standard_normal((1, d, m)) / np.sqrt(d))
+        X, W = synthetic.widen(Xb), synthetic.widen(Wb)[0]
+        Y = rmm.grouped_linear(padded(Xb, 8), padded(Wb, 8), torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    check(Y, X @ W, np.abs(X) @ np.abs(W), d, f"{n} x {d} x {m}")
+
+
+def test_all_rows_in_one_of_many_groups():
+    """An average group of one row, and one that has them all (more tiles than a launch
+    that splits the contraction takes them to be)."""
+    g = synthetic.rng(73)
+    n, d, m, E = 150, 300, 640, 150
+    X = synthetic.to_bf16(g.standard_normal((n, d)))
+    W = synthetic.to_bf16(g.standard_normal((E, d, m)))
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[78:] = n
+    Y = rmm.grouped_linear(padded(X, 8), W.cuda(), off.cuda())
+    Xw, Ww = synthetic.widen(X), synthetic.widen(W[77])
+    check(Y, Xw @ Ww, np.abs(Xw) @ np.abs(Ww), d, "one group")
+    off4 = torch.tensor([0, 0, 0, n, n], dtype=torch.int32)  # three of four groups empty
+    Y = rmm.grouped_linear(padded(X, 8), W[:4].cuda(), off4.cuda())
+    Ww = synthetic.widen(W[2])
+    check(Y, Xw @ Ww, np.abs(Xw) @ np.abs(Ww), d, "one of four")
+
+
+def test_offsets_past_32_bits():
+    """Outputs and weights of more than 2^31 elements: the last rows and the last group."""
+    n, d, m = 66000, 16, 33000
+    g = torch.Generator(device="cuda").manual_seed(74)
+    X = torch.randn((n, d), generator=g, device="cuda").bfloat16()
+    W = torch.randn((2, d, m), generator=g, device="cuda").bfloat16()
+    off = torch.tensor([0, 40000, n], dtype=torch.int32, device="cuda")
+    Y = rmm.grouped_linear(X, W, off)
+    xq, sx = rmm.quantize_fp8(X)
+    wq, sw = rmm.quantize_fp8_weight(W)
+    Yq = rmm.grouped_linear_fp8(xq, sx, wq, sw, off)
+    rows = [0, 39999, 40000, n - 1]
+    for r in rows:
+        e = int(r >= 40000)
+        x, w = wide(X[r]), wide(W[e])
+        check(Y[r], x @ w, np.abs(x) @ np.abs(w), d, f"row {r}")
+        x, w = oracle.fp8_widen(wide(xq[r:r + 1]), sx[:, r:r + 1].cpu().numpy()), oracle.fp8_widen_weight(wide(wq[e]), sw[e].cpu().numpy())
+        check(Yq[r:r + 1], x @ w, np.abs(x) @ np.abs(w), d, f"fp8 row {r}")
+    del Y, Yq
+    E, d, m = 5, 20480, 26624                       # 2.7e9 weights
+    W = torch.zeros((E, d, m), dtype=F8, device="cuda")
+    W[4, -1, -1] = 2.0
+    W[3, 0, 0] = 1.0
+    xq = torch.ones((2, d), device="cuda").to(F8)
+    sx = torch.ones((d // 128, 2), device="cuda")
+    sw = torch.ones((E, d // 128, m // 128), device="cuda")
+    off = torch.tensor([0, 0, 0, 0, 1, 2], dtype=torch.int32, device="cuda")
+    Y = rmm.grouped_linear_fp8(xq, sx, W, sw, off)
+    assert Y[0, 0] == 1 and Y[1, -1] == 2 and Y.abs().sum() == 3
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_bad_offsets_are_clamped(fp8):
     """Negative, falling and too large bounds read and write nothing out of range."""
@@ -300,6 +408,26 @@ def test_refused_shapes_and_layouts():
         rmm.linear_fp8(q, s.t(), wq[0], sw[0])
     with pytest.raises(TypeError, match="float8"):
         rmm.linear_fp8(X, s, wq[0], sw[0])
+    with pytest.raises(ValueError, match="w_scale"):
+        rmm.linear_fp8(q, s, wq[0], sw[:, 0])
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        rmm.grouped_linear(X, W, off.cpu())
+    with pytest.raises(ValueError, match="3 dimensions"):
+        rmm.grouped_linear(X, W[0], off)
+
+
+def test_one_block_scales_as_torch_lays_them_out():
+    """Scales of a single block, whose row stride torch may give as anything."""
+    g = synthetic.rng(75)
+    X = synthetic.to_bf16(g.standard_normal((40, 100)))
+    W = synthetic.to_bf16(g.standard_normal((100, 200)))
+    q, s = rmm.quantize_fp8(padded(X, 8))
+    wq, sw = rmm.quantize_fp8_weight(padded(W, 8))
+    Y = rmm.linear_fp8(q, s, wq, sw)
+    turned = s.clone().t().contiguous().t().contiguous()  # [1, 40] with strides (1, 1)
+    assert torch.equal(rmm.linear_fp8(q, turned, wq, sw), Y)
+    one = rmm.linear_fp8(q[7:8], s[:, 7:8], wq, sw)        # one row of a wider batch
+    assert torch.equal(one[0], Y[7])
 
 
 # ------------------------------------------------------------------ together, as they are used
