@@ -75,25 +75,28 @@ struct GroupedCfg {
   static constexpr int HC = COLS / 2;          // columns of one epilogue thread
   static constexpr int TMEM_COLS = 2 * COLS;
   static constexpr int SCALE_BYTES = 8 * 2 * HC * 4;
+  static constexpr int OUT_BYTES = 8 * 512;    // results on their way, 512 bytes per epilogue warp
   // OCC CTAs share an SM (with the bounds of up to 128 groups; more lower it to one)
   static constexpr int BOUND_GROUPS = OCC == 1 ? kGroupedMaxGroups : 128;
   static constexpr int STAGES_FIT =
-      (233472 / OCC - 1024 - 1024 - 256 - SCALE_BYTES - (2 * BOUND_GROUPS + 2) * 4) / (A_BYTES + X_BYTES);
+      (233472 / OCC - 1024 - 1024 - 256 - SCALE_BYTES - OUT_BYTES - (2 * BOUND_GROUPS + 2) * 4) / (A_BYTES + X_BYTES);
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static_assert(STAGES >= 3, "at least three stages");
   static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory");
   static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier area");
   static int smem_bytes(int groups) {
-    return 1024 + STAGES * (A_BYTES + X_BYTES) + SCALE_BYTES + 256 + (2 * groups + 2) * 4;
+    return 1024 + STAGES * (A_BYTES + X_BYTES) + SCALE_BYTES + OUT_BYTES + 256 + (2 * groups + 2) * 4;
   }
 };
 
 // Clamped group bounds off[0..groups] and the running count of N-row tiles
-// pre[0..groups], by one warp.
+// pre[0..groups], by the whole CTA: all bounds are fetched at once, then one warp
+// scans them, a run of neighbours per lane (fetched by the scan, 32 at a time, 114
+// groups cost 5 us).
 template <int N>
-__device__ __forceinline__ void grouped_bounds(const GroupedParams& p, int* off, int* pre, int lane) {
+__device__ __forceinline__ void grouped_bounds(const GroupedParams& p, int* off, int* pre, int warp, int lane) {
   if (p.offsets == nullptr) {
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
       off[0] = 0;
       off[1] = p.n;
       pre[0] = 0;
@@ -101,31 +104,36 @@ __device__ __forceinline__ void grouped_bounds(const GroupedParams& p, int* off,
     }
     return;
   }
-  int top = 0;   // largest bound so far
-  for (int b = 0; b <= p.groups; b += 32) {
-    int v = b + lane <= p.groups ? min(p.offsets[b + lane], p.n) : 0;
-    v = max(v, top);
+  for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) off[i] = min(max(__ldg(p.offsets + i), 0), p.n);
+  __syncthreads();
+  if (warp != 2) return;
+  const int run = (p.groups + 32) / 32;  // entries per lane of groups + 1
+  const int lo = min(lane * run, p.groups + 1), hi = min(lo + run, p.groups + 1);
+  int top = 0;  // the largest bound so far: this lane's, then with those of the lanes before
+  for (int i = lo; i < hi; ++i) top = max(top, off[i]);
 #pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const int u = __shfl_up_sync(0xffffffffu, v, s);
-      if (lane >= s) v = max(v, u);
-    }
-    if (b + lane <= p.groups) off[b + lane] = v;
-    top = __shfl_sync(0xffffffffu, v, 31);
+  for (int s = 1; s < 32; s *= 2) {
+    const int u = __shfl_up_sync(0xffffffffu, top, s);
+    if (lane >= s) top = max(top, u);
   }
-  __syncwarp();
-  int sum = 0;
-  for (int b = 0; b < p.groups; b += 32) {
-    int v = b + lane < p.groups ? (off[b + lane + 1] - off[b + lane] + N - 1) / N : 0;
+  top = __shfl_up_sync(0xffffffffu, top, 1);
+  if (lane == 0) top = 0;
+  int tiles = 0, last = top;  // of the groups that end at this lane's bounds
+  for (int i = lo; i < hi; ++i) {
+    const int v = max(off[i], last);
+    off[i] = v;
+    if (i > 0) tiles += (v - last + N - 1) / N;
+    last = v;
+    pre[i] = tiles;
+  }
+  int before = tiles;
 #pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const int u = __shfl_up_sync(0xffffffffu, v, s);
-      if (lane >= s) v += u;
-    }
-    if (b + lane < p.groups) pre[b + lane + 1] = sum + v;
-    sum += __shfl_sync(0xffffffffu, v, 31);
+  for (int s = 1; s < 32; s *= 2) {
+    const int u = __shfl_up_sync(0xffffffffu, before, s);
+    if (lane >= s) before += u;
   }
-  if (lane == 0) pre[0] = 0;
+  before -= tiles;
+  for (int i = lo; i < hi; ++i) pre[i] += before;
 }
 
 // One piece of work: rows [row0, row_end) (at most w of them) of group `group`
@@ -196,53 +204,43 @@ __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) 
                : "memory");
 }
 
-// transpose of an 8 x 8 matrix of 16-bit values held two per thread (thread T:
-// row T / 4, columns 2 (T % 4) + {0, 1})
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-  uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
-  return d;
-}
-
 // Writes an 8-row x 32-column piece of Y.  v[j]: fp32 pairs of columns T / 4 + 8 j
-// of W for rows 2 (T % 4) + {0, 1} of X.  Rounded to bf16 and transposed inside
-// the warp, each thread ends with 8 neighbouring columns of row T / 4: one
-// 16-byte store, 64 bytes of a row per four threads.
-__device__ __forceinline__ void grouped_store(const GroupedParams& p, const uint64_t (&v)[4], int row_base, int row_end,
-                                              int col_base, int lane) {
+// of W for rows 2 (T % 4) + {0, 1} of X.  Rounded to bf16 and transposed on their
+// way to 512 bytes of shared memory of this warp (`buf`), read back as 8
+// neighbouring columns of row T / 4 per thread: one 16-byte store, 64 bytes of a row
+// per four threads.  (Transposed by moves and shuffles inside the warp instead, it
+// took three times the instructions.)
+__device__ __forceinline__ void grouped_store(const GroupedParams& p, uint8_t* buf, const uint64_t (&v)[4], int row_base,
+                                              int row_end, int col_base, int lane) {
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(static_cast<uint32_t>(v[j])),
                                                    __uint_as_float(static_cast<uint32_t>(v[j] >> 32)));
-    w[j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&t));
+    w[j] = *reinterpret_cast<const uint32_t*>(&t);
   }
-  // thread q of four holds word q of each of the four 8-column blocks; it keeps
-  // its own block's: round r exchanges with thread q ^ r
-  const int q = lane & 3;
-  uint32_t o[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int j = q ^ r;
-    const uint32_t mine = j < 2 ? (j == 0 ? w[0] : w[1]) : (j == 2 ? w[2] : w[3]);
-    o[r] = r == 0 ? mine : __shfl_xor_sync(0xffffffffu, mine, r);  // word q ^ r of block q
-  }
-  uint32_t x[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = q ^ j;
-    x[j] = r < 2 ? (r == 0 ? o[0] : o[1]) : (r == 2 ? o[2] : o[3]);
-  }
-  const int row = row_base + (lane >> 2);
+  // 8 x 8 matrix j: lane 8 j + i names where its i-th row of X goes; a row's four
+  // 16-byte columns are rotated by half the row number, against bank conflicts
+  const int i = lane & 7, j = lane >> 3;
+  const uint32_t at = smem_u32(buf) + static_cast<uint32_t>(i * 64 + (((j + (i >> 1)) & 3) << 4));
+  __syncwarp();  // the last piece has been read
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3])
+               : "memory");
+  __syncwarp();
+  const int r = lane >> 2, q = lane & 3;
+  const uint4 x = lds_v4(smem_u32(buf) + static_cast<uint32_t>(r * 64 + (((q + (r >> 1)) & 3) << 4)));
+  const int row = row_base + r;
   const int col = col_base + q * 8;
   if (row < row_end && col < p.m) {
     uint16_t* y = p.Y + static_cast<int64_t>(row) * p.ldy + col;
     if (col + 8 <= p.m) {
-      *reinterpret_cast<uint4*>(y) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(y) = x;
     } else {
+      const uint32_t c[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (col + e < p.m) y[e] = static_cast<uint16_t>(x[e >> 1] >> ((e & 1) * 16));
+        if (col + e < p.m) y[e] = static_cast<uint16_t>(c[e >> 1] >> ((e & 1) * 16));
     }
   }
 }
@@ -264,7 +262,8 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
   uint8_t* sA = smem;
   uint8_t* sX = smem + STAGES * C::A_BYTES;
   float* sScale = reinterpret_cast<float*>(sX + STAGES * C::X_BYTES);  // [8 warps][2][HC]
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sScale) + C::SCALE_BYTES);  // even CTA
+  uint8_t* sOut = reinterpret_cast<uint8_t*>(sScale) + C::SCALE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);  // even CTA
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // even CTA
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
     }
   }
   wait_prior_kernels();  // bounds, operands and the output are touched only after this
-  if (warp == 2) grouped_bounds<N>(p, off, pre, lane);
+  grouped_bounds<N>(p, off, pre, warp, lane);
   tc_fence_before();
   if (CG == 2) cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
   else __syncthreads();
@@ -454,6 +453,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HC);
     const uint32_t tempty_even = CG == 2 ? map_shared_rank(smem_u32(&tempty[0]), 0u) : 0u;
     float* my_scale = sScale + (warp - 2) * 2 * HC;
+    uint8_t* out = sOut + (warp - 2) * 512;
     // this thread's sums with splits, [HC / 2][32 lanes] per warp, over the stages
     // (every copy and product of the one tile is complete when they are written)
     uint64_t* my_part = reinterpret_cast<uint64_t*>(smem) + (warp - 2) * (HC / 2) * 32 + lane;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
         }
 #pragma unroll
         for (int g = 0; g < HC / 8; ++g)
-          grouped_store(p, sum[g], t.row0 + r_of(g * 8), t.row_end, (mblock0 + mt_of(g * 8)) * 128 + quarter * 32, lane);
+          grouped_store(p, out, sum[g], t.row0 + r_of(g * 8), t.row_end, (mblock0 + mt_of(g * 8)) * 128 + quarter * 32, lane);
       } else {
         const uint32_t acc = acc_i & 1u;
         if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue, 64)) break;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
               for (int j = 0; j < 4; ++j) my_part[((c * 2 + g) * 4 + j) * 32] = v[j];
               continue;
             }
-            grouped_store(p, v, t.row0 + r_of(c * 16 + g * 8), t.row_end,
+            grouped_store(p, out, v, t.row0 + r_of(c * 16 + g * 8), t.row_end,
                           (mblock0 + mt_of(c * 16 + g * 8)) * 128 + quarter * 32, lane);
           }
         }
@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
     if (warp >= 2 && worker < units.count) {
       const GroupedTile t = units.get(worker);
       const int quarter = warp & 3, half = (warp - 2) >> 2;
+      uint8_t* out = sOut + (warp - 2) * 512;
       const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((((warp - 2) * (HC / 2)) * 32 + lane) * 8);
 #pragma unroll
       for (int g = 0; g < HC / 8; ++g) {
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
         const int i = g * 8;
         const int mt = HC >= N ? half * (HC / N) + i / N : 0;
         const int row = HC >= N ? i % N : half * HC + i;
-        grouped_store(p, v, t.row0 + row, t.row_end, (t.mtile * MT + mt) * 128 + quarter * 32, lane);
+        grouped_store(p, out, v, t.row0 + row, t.row_end, (t.mtile * MT + mt) * 128 + quarter * 32, lane);
       }
     }
   }

@@ -17,7 +17,7 @@
 // out of tensor memory before it adds the last ones of this block.
 //
 // Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers (even CTA),
-// one for each product, warp 3 the group bounds, warps 4-11 epilogue: warp w reads
+// one for each product, warps 4-11 epilogue: warp w reads
 // lanes 32 (w % 4) .. + 31 of one of the two products.  The columns of product h
 // are two runs, one from each CTA's half of the tile: [h w / 4, (h + 1) w / 4) and
 // w / 2 further, w the tile's columns.  Results go through 4 KB of shared memory
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     tmem_relinquish_pair();
   }
   wait_prior_kernels();  // bounds, operands and the output are touched only after this
-  if (warp == 3) grouped_bounds<256>(p, off, pre, lane);
+  grouped_bounds<256>(p, off, pre, warp, lane);
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
   tc_fence_after();
