@@ -21,7 +21,8 @@
 // lanes 32 (w % 4) .. + 31 of one of the two products.  The columns of product h
 // are two runs, one from each CTA's half of the tile: [h w / 4, (h + 1) w / 4) and
 // w / 2 further, w the tile's columns.  Results go through 4 KB of shared memory
-// per warp, so that a store writes 128 bytes of a row and not 16.
+// per warp: 32 rows that all belong to the group leave as one TMA store of 64
+// columns, others row by row, 128 bytes at a time.
 // The tiles of a partial last wave are cut along W into 128- or 64-column pieces.
 #pragma once
 #include "grouped.cuh"
@@ -37,7 +38,7 @@ struct GroupedFp8Cfg {
   // registers per thread at launch, and the split after the set-up: 128 sums and
   // two 32-column loads in flight per epilogue thread (the host checks that the
   // kernel was compiled to LAUNCH_REGS, on which the split draws)
-  static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 56, EPI_REGS = 224;
+  static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 40, EPI_REGS = 232;
   static_assert(OTHER_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "three warpgroups share what was launched");
   static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + OUT_BYTES + 256 + (2 * groups + 2) * 4; }
   static_assert(8 * (2 * STAGES + 9) + 8 <= 256, "barrier area");
@@ -111,7 +112,7 @@ struct GroupedFp8Units {
 
 __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     grouped_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                            const GroupedParams p) {
+                            const __grid_constant__ CUtensorMap tmY, const GroupedParams p) {
   using C = GroupedFp8Cfg;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t grouped_fp8_smem_raw[];
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     fence_barrier_init();
     prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmY);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -265,12 +267,12 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     uint8_t* out = sOut + (warp - 4) * 4096;
     uint32_t acc_i = 0;
     bool ok = true;
-    // the tile at hand; the row's scales of the next two blocks and where the one
-    // after stands; the weight blocks' scales of 32 blocks, one per lane (uniform
-    // over the warp, they are passed on by shuffles: two loads a block less)
+    // the tile at hand; the scales of its next block (s0, s1) and the row's of the two
+    // after; the weight blocks' scales of 32 blocks and of the 32 after, one per lane
+    // (uniform over the warp, they are passed on by shuffles: two loads a block less)
     GroupedTile t;
     const float *px = nullptr, *pu = nullptr, *pv = nullptr;
-    float x0, x1, u32, v32;
+    float s0, s1, x1, x2, u, v, u_next, v_next;
     auto next_x = [&](int kb) {  // of block kb; past the last one its own again
       const float x = ldg_f32_pinned(px);
       px += kb + 1 < p.num_kb ? p.lds : 0;
@@ -278,8 +280,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     };
     auto load_w = [&](int kb) {  // of blocks kb .. kb + 31
       const int64_t at = static_cast<int64_t>(min(kb + lane, p.num_kb - 1)) * p.sw_cols;
-      u32 = ldg_f32_pinned(pu + at);
-      v32 = ldg_f32_pinned(pv + at);
+      u_next = ldg_f32_pinned(pu + at);
+      v_next = ldg_f32_pinned(pv + at);
     };
     auto begin = [&](int unit) {
       t = units.get(unit);
@@ -290,12 +292,18 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       const int col0 = t.mtile + half * (t.w / 4);
       pu = sw + min(col0 / 128, p.sw_cols - 1);
       pv = sw + min((col0 + t.w / 2) / 128, p.sw_cols - 1);
-      x0 = next_x(0);
+      s0 = next_x(0);
       x1 = next_x(1);
+      x2 = next_x(2);
       load_w(0);
     };
     if (worker < units.count) begin(worker);
     for (int unit = worker; unit < units.count; unit += workers) {
+      u = u_next;
+      v = v_next;
+      s1 = s0 * __shfl_sync(0xffffffffu, v, 0);
+      s0 *= __shfl_sync(0xffffffffu, u, 0);
+      if (p.num_kb > 32) load_w(32);
       float sum[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
@@ -307,10 +315,12 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       for (int kb = 0; ok && kb < p.num_kb; ++kb) {
         const uint32_t acc = acc_i & 1u;
         ++acc_i;
-        const float s0 = x0 * __shfl_sync(0xffffffffu, u32, kb & 31), s1 = x0 * __shfl_sync(0xffffffffu, v32, kb & 31);
-        x0 = x1;
-        x1 = next_x(kb + 2);
-        if ((kb & 31) == 31) load_w(kb + 1);
+        if ((kb & 31) == 31) {
+          u = u_next;
+          v = v_next;
+          if (kb + 33 < p.num_kb) load_w(kb + 33);
+        }
+        float s0_next = 0.f, s1_next = 0.f;
         // 16 columns at a time, the next 16 on their way (a narrow piece reads past
         // its columns, inside the accumulator; those sums are not stored).  The
         // loads stand outside every branch, and the additions keep their place:
@@ -322,11 +332,17 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           tmem_ld_wait();
           if (c < 7) {
             tmem_ld16(base + acc * 256 + (c + 1) * 16, r[(c + 1) & 1]);
+            if (c == 1) s0_next = x1 * __shfl_sync(0xffffffffu, u, (kb + 1) & 31);
+            if (c == 2) s1_next = x1 * __shfl_sync(0xffffffffu, v, (kb + 1) & 31);
+            if (c == 3) {
+              x1 = x2;
+              x2 = next_x(kb + 3);
+            }
           } else {
             tc_fence_before();
             __syncwarp();
             if (elect_one()) mbar_arrive_cluster_relaxed(tempty_even + 8u * (acc * 2 + half));
-            if (!ready && kb + 1 < p.num_kb)
+            if (kb + 1 < p.num_kb && __any_sync(0xffffffffu, !ready))
               ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
             tc_fence_after();
             tmem_ld16(base + (acc ^ 1u) * 256, r[0]);  // (after the last block: not used)
@@ -337,6 +353,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
             if (c != 5) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), c < 4 ? s0 : s1);
           }
         }
+        s0 = s0_next;
+        s1 = s1_next;
       }
       tmem_ld_wait();
       if (!ok) break;
@@ -345,10 +363,15 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       const int skip = t.w / 2 - run;
       const int row0 = t.row0 + static_cast<int>(rank) * 128 + quarter * 32;
       const int row_end = t.row_end;
-      if (unit + workers < units.count) begin(unit + workers);  // its scales come while this tile is written
+      const bool whole = t.w == 256 && row0 + 32 <= row_end;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {  // accumulator columns 64 q .. 64 q + 63
-        if (q * 64 >= 2 * run) break;
+        if (q == 1) {
+          // the next tile's scales come while this one is written
+          if (unit + workers < units.count) begin(unit + workers);
+          if (64 >= 2 * run) break;
+        }
+        if (lane == 0) bulk_wait_group_read<0>();  // the last store has left the buffer
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -359,6 +382,16 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
             w[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
           *reinterpret_cast<uint4*>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int col = col0 + q * (64 + skip);  // run = 64
+          if (lane == 0 && col < p.m) {
+            tma_store_3d(&tmY, out, col, row0, 0);
+            bulk_commit_group();
+          }
+          continue;
         }
         __syncwarp();
         const int k = lane & 7;              // 8 columns of this thread's rows lane / 8, + 4, ...
@@ -383,6 +416,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
         }
       }
     }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
   }
 
   tc_fence_before();

@@ -1988,6 +1988,10 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   CUtensorMap tw, tx;
   if (rmm_status st = make_tmaps_grouped(&tw, &tx, true, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx, 128))
     return st;
+  CUtensorMap ty;
+  if (rmm_status st = make_tmap_out(&ty, c.p.Y, false, static_cast<uint64_t>(c.m), static_cast<uint64_t>(c.n), 1,
+                                    static_cast<uint64_t>(c.p.ldy), 0))
+    return st;
   GroupedParams p = c.p;
   p.num_kb = static_cast<int>(ceil_div(c.d, 128));
   p.m_tiles = static_cast<int>(ceil_div(c.m, 256));
@@ -2006,7 +2010,7 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   if (regs != GroupedFp8Cfg::LAUNCH_REGS)
     return fail(RMM_ERR_CUDA, "grouped fp8 kernel compiled to %d registers, not %d", regs, GroupedFp8Cfg::LAUNCH_REGS);
   e = launch_cluster(grouped_fp8_rows_kernel, dim3(static_cast<unsigned>(workers * 2)), dim3(GroupedFp8Cfg::THREADS), smem, 2,
-                     s, tw, tx, p);
+                     s, tw, tx, ty, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return RMM_OK;
 }
