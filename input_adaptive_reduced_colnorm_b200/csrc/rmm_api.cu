@@ -1960,15 +1960,18 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   const int64_t row_tiles = ceil_div(c.n, N) + std::min<int64_t>(c.groups - 1, c.n);
   // (a tile of the last wave may be cut into up to eight)
   if (8 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
-  // Few tiles: split each one's contraction over a cluster of 2 or 4 so that about
-  // every SM has a part (clusters of 4 reached 132 of 148 SMs; clusters of 8 only
-  // 120, and at n = 1, 4096 x 4096 e4m3 they took 9.0 us, those of 4 7.6 us, no
-  // split 13.6 us).  A launch has a cluster for every tile that there may be.
+  // Few tiles: split each one's contraction over a cluster so that about every SM has
+  // a part (n = 1, 4096 x 4096 e4m3: 13.6 us whole, 7.6 us with clusters of 4).
+  // Clusters of 4 reach 132 of 148 SMs and those of 8 only 120, and theirs cost more
+  // to gather (the same call with clusters of 8: 9.0 us), so they are left to calls of
+  // few and long tiles (7 x 11200 x 246 of 3 groups: 11.5 us against 16.2 with 4).
+  // A launch has a cluster for every tile that there may be.
   int64_t splits = 1;
   if (CG == 1) {
     const int64_t tiles = grouped_tiles(c, N, MT * 128);
     if (2 * tiles <= num_sms() * OCC && p.num_kb >= 2) splits = 2;
     if (4 * tiles <= (num_sms() - 16) * OCC && p.num_kb >= 4) splits = 4;
+    if (8 * tiles <= 2 * num_sms() / 3 && p.num_kb >= 32) splits = 8;
   }
   p.splits = static_cast<int>(splits);
   const int64_t workers = splits > 1 ? row_tiles * p.m_tiles : std::min<int64_t>((N >= 128 ? N / 32 : 1) * row_tiles * p.m_tiles, std::max(1, num_sms() * OCC / CG));
@@ -2024,7 +2027,10 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
 //     epilogue 0.45 us (1 x 4096 x 14336: 17.3 against 14.9).
 //   16 x 256, two CTAs per SM, up to 16 rows: e4m3 256 x 2048 x 1536 of 128 groups
 //     57 against 59 with 16 x 512 and one CTA.
-//   32 x 512 up to 32 rows: e4m3 256 x 4096 x 14336 of 8 81 against 85 with 16 rows.
+//   32 x 256 up to 32 rows: 2400 x 2048 x 1408 of 100 groups 91 against 95 with 16 or
+//     64 rows, or 512 columns; e4m3 32 x 512, whose blocks are half as long to load:
+//     54 against 59 with 256 columns and 60 with 64 rows, but not for a matrix of one
+//     such tile (1989 x 8330 x 218 of 120: 71 against 49 with 64 rows).
 //   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
 //     83 with 32; e4m3 up to 128 rows: 128 x 4096 x 14336 22 against 23 with 256 rows.
 //   256 x 256 on CTA pairs for more, unless their tiles leave most SMs idle (256 x
@@ -2035,7 +2041,7 @@ rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   const int64_t small = grouped_tiles(c, 32, 128);
   if (small <= num_sms() && (!FP8 || 2 * small <= num_sms() || c.d <= 2048)) return launch_grouped_t<FP8, 32, 1, 1>(c, s);
   if (rows <= 16) return launch_grouped_t<FP8, 16, 2, 1, 2>(c, s);
-  if (rows <= 32) return launch_grouped_t<FP8, 32, 4, 1>(c, s);
+  if (rows <= 32 && (!FP8 || c.m > 256)) return launch_grouped_t<FP8, 32, FP8 ? 4 : 2, 1>(c, s);
   if (rows <= (FP8 ? 128 : 64) || 5 * grouped_tiles(c, 256, 256) < num_sms()) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
   if constexpr (FP8) return launch_grouped_fp8_rows(c, s);
   else return launch_grouped_t<false, 256, 1, 2>(c, s);
