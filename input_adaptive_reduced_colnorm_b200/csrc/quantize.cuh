@@ -4,11 +4,12 @@
 // Activations: blocks of 1 row x 128 columns (quantize_rows_kernel); weights:
 // blocks of 128 x 128 (quantize_blocks_kernel).
 //
-// Bound by memory (2 bytes read, 1 written per element) as long as the
-// instructions per element stay near 5: a first version (one IEEE division per
-// scale, scalar arithmetic, 16 lanes per block) was bound by issue slots at 58 %
-// of the copy bandwidth.  Each element is read once and stays in registers between
-// the maximum and the division.
+// Bound by memory (2 bytes read, 1 written per element): 8192 x 14336 takes 55 us,
+// 0.98 of the copy bandwidth, eight 4096 x 14336 weights 213 us, 0.99.  It takes about
+// 10 instructions per element to stay there (packed arithmetic, 8 lanes a block, 32-bit
+// columns, no edge checks where d is a multiple of 16): with 14 the same call took
+// 63 us, with IEEE divisions and 16 lanes a block 94 us, bound by issue slots.  Each
+// element is read once and stays in registers between the maximum and the division.
 //
 // The division, on packed pairs: q0 = x r, q = q0 + (x - q0 s) r with r ~ 1 / s
 // (Markstein 1990) has a relative error below 2^-44 before its last rounding.
@@ -106,83 +107,95 @@ struct QuantDiv {
   }
 };
 
-// 8 bf16 at x, the first `left` of which exist (others read as zero)
-__device__ __forceinline__ uint4 quant_load8(const uint16_t* x, int64_t left) {
-  if (left >= 8) return ldg_nc_v4(x);
+// 8 bf16 at x, of which `left` exist (others read as zero); WHOLE: all or none
+template <bool WHOLE>
+__device__ __forceinline__ uint4 quant_load8(const uint16_t* x, int left) {
+  if (WHOLE ? left > 0 : left >= 8) return ldg_nc_v4(x);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (!WHOLE) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < left) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + e)) << ((e & 1) * 16);
+    for (int e = 0; e < 7; ++e)
+      if (e < left) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + e)) << ((e & 1) * 16);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void quant_store16(uint8_t* q, const uint4& v, int64_t left) {
-  if (left >= 16) {
+// the first `left` of 16 e4m3
+template <bool WHOLE>
+__device__ __forceinline__ void quant_store16(uint8_t* q, const uint4& v, int left) {
+  if (WHOLE ? left > 0 : left >= 16) {
     *reinterpret_cast<uint4*>(q) = v;
-    return;
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  } else if (!WHOLE && left > 0) {
+    uint32_t lo = v.x, hi = v.y;
+    if (left >= 8) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(v.x, v.y);
+      q += 8;
+      left -= 8;
+      lo = v.z;
+      hi = v.w;
+    }
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e < left) q[e] = static_cast<uint8_t>(w[e >> 2] >> ((e & 3) * 8));
+    for (int e = 0; e < 7; ++e)
+      if (e < left) q[e] = static_cast<uint8_t>((e < 4 ? lo : hi) >> ((e & 3) * 8));
+  }
 }
 
 // A team of 8 lanes takes a block of one row, 16 columns per lane; a warp four
 // neighbouring blocks (1 KB of the row), U times.  R = 8: the warps of a CTA take
 // 8 consecutive rows, whose scales are neighbours in memory; R = 1 (few rows): they
-// take consecutive blocks of one row.
-template <int R, int U>
+// take consecutive blocks of one row.  WHOLE: d is a multiple of 16, so that a lane
+// has 16 columns or none.
+template <int R, int U, bool WHOLE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
   constexpr int WB = 8 / R;               // warps side by side along the blocks
   constexpr int CHUNK = WB * 4 * U;       // blocks of one row in a CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tl = lane & 7;
-  const int64_t blocks = (p.d + 127) / 128;
-  const int64_t chunks = (blocks + CHUNK - 1) / CHUNK;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) / chunks * R + warp / WB;
-  const int64_t b0 = static_cast<int64_t>(blockIdx.x) % chunks * CHUNK + (warp % WB) * 4 * U + (lane >> 3);
+  const int d = static_cast<int>(p.d);
+  const unsigned chunks = (static_cast<unsigned>(d) + CHUNK * 128 - 1) / (CHUNK * 128);
+  const int64_t row = static_cast<int64_t>(blockIdx.x / chunks) * R + warp / WB;
   if (row >= p.n) return;
+  const int b0 = static_cast<int>(blockIdx.x % chunks) * CHUNK + (warp % WB) * 4 * U + (lane >> 3);
+  const int left = d - (b0 * 128 + tl * 16);  // columns from this lane's first on
+  const uint16_t* x = p.x + row * p.ldx + b0 * 128 + tl * 16;
+  uint8_t* q = p.q + row * p.ldq + b0 * 128 + tl * 16;
+  float* s = p.s + b0 * p.lds + row;
   wait_prior_kernels();
-  const uint16_t* x = p.x + row * p.ldx;
   uint4 v[U][2];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t col = (b0 + u * 4) * 128 + tl * 16 + h * 8;
-      v[u][h] = col < p.d ? quant_load8(x + col, p.d - col) : make_uint4(0u, 0u, 0u, 0u);
-    }
+  for (int u = 0; u < U; ++u) {
+    v[u][0] = quant_load8<WHOLE>(x + u * 512, left - u * 512);
+    v[u][1] = quant_load8<WHOLE>(x + u * 512 + 8, left - u * 512 - 8);
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     uint32_t m = absmax_words(v[u][1], absmax_words(v[u][0], 0u));
 #pragma unroll
     for (int k = 4; k >= 1; k /= 2) m = absmax_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, k));
     const QuantDiv dv(absmax_value(m));
-    const int64_t blk = b0 + u * 4;
-    const int64_t col = blk * 128 + tl * 16;
-    if (col < p.d) quant_store16(p.q + row * p.ldq + col, dv.sixteen(v[u][0], v[u][1]), p.d - col);
-    if (tl == 0 && blk < blocks) p.s[blk * p.lds + row] = dv.s;
+    quant_store16<WHOLE>(q + u * 512, dv.sixteen(v[u][0], v[u][1]), left - u * 512);
+    if (tl == 0 && left > u * 512) s[u * 4 * p.lds] = dv.s;
   }
 }
 
 // One 128 x 128 block per CTA: 32 rows per pass, 8 lanes x 16 columns per row.
+template <bool WHOLE>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const QuantParams p) {
   __shared__ uint32_t warp_max[8];
-  const int64_t blk = blockIdx.x;
-  const int mb = static_cast<int>(blk % p.mblocks);
-  const int64_t rest = blk / p.mblocks;
-  const int db = static_cast<int>(rest % p.dblocks);
-  const int64_t mat = rest / p.dblocks;
-  const int64_t row0 = static_cast<int64_t>(db) * 128 + (threadIdx.x >> 3);
-  const int64_t col = static_cast<int64_t>(mb) * 128 + (threadIdx.x & 7) * 16;
+  const unsigned blk = blockIdx.x;
+  const unsigned mb = blk % static_cast<unsigned>(p.mblocks), rest = blk / static_cast<unsigned>(p.mblocks);
+  const unsigned db = rest % static_cast<unsigned>(p.dblocks), mat = rest / static_cast<unsigned>(p.dblocks);
+  const int row0 = static_cast<int>(db) * 128 + (threadIdx.x >> 3);
+  const int col = static_cast<int>(mb) * 128 + (threadIdx.x & 7) * 16;
+  const int rows = static_cast<int>(p.n), left = static_cast<int>(p.d) - col;
   const uint16_t* x = p.x + mat * p.xstride + row0 * p.ldx + col;
   uint8_t* q = p.q + mat * p.qstride + row0 * p.ldq + col;
   wait_prior_kernels();
   uint4 v[4][2];
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      v[u][h] = (row0 + u * 32 < p.n && col + h * 8 < p.d) ? quant_load8(x + u * 32 * p.ldx + h * 8, p.d - col - h * 8)
-                                                           : make_uint4(0u, 0u, 0u, 0u);
+  for (int u = 0; u < 4; ++u) {
+    const int here = row0 + u * 32 < rows ? left : 0;
+    v[u][0] = quant_load8<WHOLE>(x + u * 32 * p.ldx, here);
+    v[u][1] = quant_load8<WHOLE>(x + u * 32 * p.ldx + 8, here - 8);
+  }
   uint32_t m = 0u;
 #pragma unroll
   for (int u = 0; u < 4; ++u) m = absmax_words(v[u][1], absmax_words(v[u][0], m));
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const QuantParams 
   const QuantDiv dv(absmax_value(m));
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    if (row0 + u * 32 < p.n && col < p.d) quant_store16(q + u * 32 * p.ldq, dv.sixteen(v[u][0], v[u][1]), p.d - col);
+    quant_store16<WHOLE>(q + u * 32 * p.ldq, dv.sixteen(v[u][0], v[u][1]), row0 + u * 32 < rows ? left : 0);
   if (threadIdx.x == 0) p.s[blk] = dv.s;
 }
 

@@ -2131,13 +2131,14 @@ rmm_status rmm_quantize_fp8(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx
   const int64_t blocks = ceil_div(d, 128);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  const bool whole = d % 16 == 0;
   if (n < 64) {
     const int64_t grid = n * ceil_div(blocks, 32);
-    e = launch_chained(quantize_rows_kernel<1, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    e = launch_chained(whole ? quantize_rows_kernel<1, 1, true> : quantize_rows_kernel<1, 1, false>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
   } else {
     const int64_t grid = ceil_div(n, 8) * ceil_div(blocks, 8);
     if (grid > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many blocks");
-    e = launch_chained(quantize_rows_kernel<8, 2>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
+    e = launch_chained(whole ? quantize_rows_kernel<8, 2, true> : quantize_rows_kernel<8, 2, false>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
   }
   if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
   return RMM_OK;
@@ -2173,7 +2174,7 @@ rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_
   p.qstride = q_stride;
   p.dblocks = static_cast<int>(db);
   p.mblocks = static_cast<int>(mb);
-  const cudaError_t e = launch_chained(quantize_blocks_kernel, dim3(static_cast<unsigned>(groups * db * mb)), dim3(256), 0,
+  const cudaError_t e = launch_chained(m % 16 == 0 ? quantize_blocks_kernel<true> : quantize_blocks_kernel<false>, dim3(static_cast<unsigned>(groups * db * mb)), dim3(256), 0,
                                        static_cast<cudaStream_t>(stream), p);
   if (e != cudaSuccess) return cuda_fail(e, "quantise launch");
   return RMM_OK;
