@@ -24,6 +24,11 @@
 // own: 1 MB of shared-memory reads per 256 x 256 block and SM pair, twice the
 // time of the block's tensor work; 380 TFLOP/s at 4096 x 4096 x 14336.)
 //
+// Bound by HBM with few rows (bf16 64 x 4096 x 14336 of 8 groups: 139 us, the copy
+// bandwidth; e4m3 8 x 8192 x 28672: 39 us, 0.92 of it) and by the tensor cores at the
+// power cap with many (8192 x 4096 x 14336 of 8: 685-855 us, 530 cycles a stage of
+// 512 at 1.3-1.45 GHz).
+//
 // Tiles are cut to the rows that are there: the N of a tile's instructions is
 // its row count rounded up to 16 (32 for a pair).  When the tiles do not fill a
 // whole number of waves, those of the last wave are cut into narrower ones.

@@ -16,6 +16,11 @@
 // and waits while the other multiplies); each takes the next block's first columns
 // out of tensor memory before it adds the last ones of this block.
 //
+// 4096 x 4096 x 14336: 242-276 us, 1740-1990 TFLOP/s at 1.5-1.6 GHz (the power cap).
+// Bound by the accumulators' round trip (product, commit, epilogue, hand-back: ~1500
+// cycles on two accumulators of 256 columns, all that tensor memory holds) and the
+// epilogue's steps: ~770 cycles a block where the product takes 512, and ~2500 a tile.
+//
 // Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers (even CTA),
 // one for each product, warps 4-11 epilogue: warp w reads
 // lanes 32 (w % 4) .. + 31 of one of the two products.  The columns of product h
