@@ -283,7 +283,7 @@ rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_
 
 /* rmm_linear_fp8: Y = X W on quantised operands,
  *   Y[i, c] = sum_b sx[b][i] sw[b][c / 128] sum_{j in block b} Xq[i, j] Wq[j, c],
- * the inner sums and the outer one in fp32, one rounding to bf16.
+ * the two scales multiplied first; all of it in fp32, one rounding to bf16.
  *   Xq, sx  as rmm_quantize_fp8 writes them (any scales may be used).
  *   Wq      device e4m3 [d][ldw], ldw >= m, a multiple of 16 (contraction index as the row).
  *   sw      device fp32 [ceil(d / 128)][ceil(m / 128)].

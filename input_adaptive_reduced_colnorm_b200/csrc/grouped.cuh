@@ -109,7 +109,7 @@ __device__ __forceinline__ void grouped_bounds(const GroupedParams& p, int* off,
     }
     return;
   }
-  for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) off[i] = min(max(__ldg(p.offsets + i), 0), p.n);
+  for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) off[i] = min(max(p.offsets[i], 0), p.n);
   __syncthreads();
   if (warp != 2) return;
   const int run = (p.groups + 32) / 32;  // entries per lane of groups + 1
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
             const int row = t.row0 + r_of(i * 32 + lane);
             const int mb = mblock0 + mt_of(i * 32 + lane);
             const bool there = i * 32 + lane < HC && row < t.row_end && mb < p.sw_cols;
-            nx[i] = there ? __ldg(p.sx + kb * p.lds + row) : 0.f;
-            nw[i] = there ? __ldg(p.sw + (static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb) : 0.f;
+            nx[i] = there ? p.sx[kb * p.lds + row] : 0.f;
+            nw[i] = there ? p.sw[(static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb] : 0.f;
           }
         };
         load_scales(kb_begin);

@@ -26,8 +26,8 @@
 // lanes 32 (w % 4) .. + 31 of one of the two products.  The columns of product h
 // are two runs, one from each CTA's half of the tile: [h w / 4, (h + 1) w / 4) and
 // w / 2 further, w the tile's columns.  Results go through 4 KB of shared memory
-// per warp: 32 rows that all belong to the group leave as one TMA store of 64
-// columns, others row by row, 128 bytes at a time.
+// per warp: 32 rows x 64 columns that all belong to the group and the matrix leave as
+// one TMA store, others row by row, 128 bytes at a time.
 // The tiles of a partial last wave are cut along W into 128- or 64-column pieces.
 #pragma once
 #include "grouped.cuh"
@@ -279,14 +279,14 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     const float *px = nullptr, *pu = nullptr, *pv = nullptr;
     float s0, s1, x1, x2, u, v, u_next, v_next;
     auto next_x = [&](int kb) {  // of block kb; past the last one its own again
-      const float x = ldg_f32_pinned(px);
+      const float x = ld_f32_pinned(px);
       px += kb + 1 < p.num_kb ? p.lds : 0;
       return x;
     };
     auto load_w = [&](int kb) {  // of blocks kb .. kb + 31
       const int64_t at = static_cast<int64_t>(min(kb + lane, p.num_kb - 1)) * p.sw_cols;
-      u_next = ldg_f32_pinned(pu + at);
-      v_next = ldg_f32_pinned(pv + at);
+      u_next = ld_f32_pinned(pu + at);
+      v_next = ld_f32_pinned(pv + at);
     };
     auto begin = [&](int unit) {
       t = units.get(unit);
@@ -388,12 +388,13 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           }
           *reinterpret_cast<uint4*>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (whole) {
+        // (a store that crosses column m would write zeros up to the next 16 bytes)
+        const int first = col0 + q * (64 + skip);  // where run = 64
+        if (whole && first + 64 <= p.m) {
           fence_proxy_async_smem();
           __syncwarp();
-          const int col = col0 + q * (64 + skip);  // run = 64
-          if (lane == 0 && col < p.m) {
-            tma_store_3d(&tmY, out, col, row0, 0);
+          if (lane == 0) {
+            tma_store_3d(&tmY, out, first, row0, 0);
             bulk_commit_group();
           }
           continue;

@@ -478,10 +478,21 @@ __device__ __forceinline__ void set_max_regs_up() {
 }
 
 // ---------------------------------------------------------------- misc loads
-// A load that stays where it is written (a plain one may be moved down to its use).
-__device__ __forceinline__ float ldg_f32_pinned(const float* p) {
+// Loads of what an earlier kernel may have written while this one was already
+// resident (see wait_prior_kernels): not through the non-coherent path, whose data may
+// not change during a kernel.  The pinned one stays where it is written (a plain load
+// may be moved down to its use).
+__device__ __forceinline__ float ld_f32_pinned(const float* p) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_v4_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {

@@ -110,12 +110,12 @@ struct QuantDiv {
 // 8 bf16 at x, of which `left` exist (others read as zero); WHOLE: all or none
 template <bool WHOLE>
 __device__ __forceinline__ uint4 quant_load8(const uint16_t* x, int left) {
-  if (WHOLE ? left > 0 : left >= 8) return ldg_nc_v4(x);
+  if (WHOLE ? left > 0 : left >= 8) return ld_v4_once(x);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
   if (!WHOLE) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
-      if (e < left) w[e >> 1] |= static_cast<uint32_t>(__ldg(x + e)) << ((e & 1) * 16);
+      if (e < left) w[e >> 1] |= static_cast<uint32_t>(x[e]) << ((e & 1) * 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }

@@ -232,6 +232,8 @@ def test_every_tile_shape(sizes, d, m, fp8):
         X, W = synthetic.widen(Xb), synthetic.widen(Wb)
         Y = rmm.grouped_linear(padded(Xb, 8, extra=1), padded(Wb, 8), off.cuda(), out=out)
     again = Y.clone()
+    behind = out.as_strided((n, out.stride(0)), (out.stride(0), 1))[:, m:]
+    assert behind.isnan().all()  # the buffer's columns past m are as they were
     ref = oracle.grouped_product(X, W, off.numpy(), np.full((n, m), 3.0))
     mag = oracle.grouped_product(np.abs(X), [np.abs(w) for w in W], off.numpy(), np.zeros((n, m)))
     check(Y, ref, mag, d, f"{sizes} {d} x {m}")
@@ -486,6 +488,41 @@ def test_moe_block_in_fp8_and_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(Y, eager[s - 1])
+    del graph
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_tiles_captured(fp8):
+    """The CTA-pair tiles in a graph: a replay on other rows, other group bounds and (fp8)
+    other scales, all written by kernels just before it, equals an eager call."""
+    g = synthetic.rng(69)
+    n, d, m, E = 700, 256, 2600, 2
+    W = synthetic.to_bf16(g.standard_normal((E, d, m)) / 16).cuda()
+    wq, sw = rmm.quantize_fp8_weight(W)
+    X = torch.empty((n, d), dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 300, n], dtype=torch.int32, device="cuda")
+    out = torch.zeros((n, m), dtype=torch.bfloat16, device="cuda")
+
+    def call(out=None):
+        if fp8:
+            return rmm.grouped_linear_fp8(*rmm.quantize_fp8(X), wq, sw, off, out=out)
+        return rmm.grouped_linear(X, W, off, out=out)
+
+    inputs = [(synthetic.to_bf16(4.0 ** k * g.standard_normal((n, d))).cuda(), 100 + 211 * k) for k in range(3)]
+    eager = []
+    for x, cut in inputs:
+        X.copy_(x)
+        off[1] = cut
+        eager.append(call())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    for k in (0, 1, 2, 1):
+        X.copy_(inputs[k][0])
+        off[1] = inputs[k][1]
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, eager[k])
     del graph
 
 
