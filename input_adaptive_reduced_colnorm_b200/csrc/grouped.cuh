@@ -42,10 +42,10 @@
 // clamps them to 0 <= ... <= n, non-decreasing, and sums the row tiles of the
 // groups before it starts; a tile number is looked up by bisection.
 //
-// Roles (320 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
-// epilogue.  CG = 2: two CTAs of a cluster form one M = 256 product (256 columns
-// of W x 256 rows of X), each staging its own 128 columns of W and half of the
-// rows.
+// Roles (320 threads, e4m3 352): warp 0 TMA producer, warp 1 (and for e4m3 warp 10)
+// MMA issuer, warps 2-9 epilogue.  CG = 2: two CTAs of a cluster form one M = 256
+// product (256 columns of W x 256 rows of X), each staging its own 128 columns of W
+// and half of the rows.
 #pragma once
 #include <cuda_bf16.h>
 #include "ptx.cuh"
@@ -53,7 +53,7 @@
 namespace rmm {
 
 constexpr int kGroupedMaxGroups = 1024;
-constexpr int kGroupedThreads = 320;
+constexpr int grouped_threads(bool fp8) { return fp8 ? 352 : 320; }
 
 struct GroupedParams {
   const int32_t* offsets;  // [groups + 1] on the device, or null: one group of n rows
@@ -251,7 +251,7 @@ __device__ __forceinline__ void grouped_store(const GroupedParams& p, uint8_t* b
 }
 
 template <bool FP8, int N, int MT, int CG, int OCC>
-__global__ void __launch_bounds__(kGroupedThreads, OCC)
+__global__ void __launch_bounds__(grouped_threads(FP8), OCC)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const GroupedParams p) {
   using C = GroupedCfg<N, MT, CG, OCC>;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 8 * CG);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, FP8 ? 2 : 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -373,8 +373,12 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (even CTA)
+  } else if (warp == 1 || warp == 10) {
+    // ------------------------------------------------------------ MMA issuers (even CTA)
+    // e4m3: warp 1 issues the even blocks' products, warp 10 the odd ones', each to an
+    // accumulator of its own.  Issuing takes about as long as the products, and one
+    // warp's waits between them (accumulator, operands: 400 cycles a block) would leave
+    // the tensor cores idle.  bf16 adds to one accumulator and waits once a tile.
     // The warp runs the loop together and elects the issuing lane: the descriptors
     // then stay in uniform registers (with one lane in the loop an instruction took
     // 90 cycles to issue, with the warp 20).
@@ -390,6 +394,20 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
         const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(w >> 3) << 17);
         for (int kb = kb_begin; kb < kb_end; ++kb) {
           const uint32_t acc = acc_i & 1u;
+          if (FP8 && acc != (warp == 1 ? 0u : 1u)) {  // the other warp's
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            ++acc_i;
+            continue;
+          }
+          // The accumulator first: once the epilogue has handed back block kb - 2's, every
+          // block up to it has been loaded and read, block kb - STAGES among them, so that
+          // the stage's barrier is in this block's phase or past it when it is asked.  (A
+          // warp that skips blocks and asks the stage first may meet the phase before the
+          // last, whose parity is the same.)
+          static_assert(STAGES > 2, "the stage's last block is before kb - 2");
           bool go = true;
           if (FP8 || kb == kb_begin)
             go = mbar_wait(&tempty[acc], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0,
@@ -484,10 +502,10 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
 #pragma unroll
           for (int j = 0; j < 4; ++j) sum[g][j] = 0;
         // scales of this warp's HC rows (lane, lane + 32, ...) and of the weight
-        // blocks, loaded one block ahead
+        // blocks, loaded two blocks ahead (a trip to L2 takes longer than a block)
         constexpr int SC = (HC + 31) / 32;
-        float nx[SC], nw[SC];
-        auto load_scales = [&](int kb) {
+        float nx[2][SC], nw[2][SC];
+        auto load_scales = [&](int kb, float (&nx)[SC], float (&nw)[SC]) {
 #pragma unroll
           for (int i = 0; i < SC; ++i) {
             const int row = t.row0 + r_of(i * 32 + lane);
@@ -497,19 +515,17 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
             nw[i] = there ? p.sw[(static_cast<int64_t>(t.group) * p.num_kb + kb) * p.sw_cols + mb] : 0.f;
           }
         };
-        load_scales(kb_begin);
-        for (int kb = kb_begin; kb < kb_end; ++kb, ++acc_i) {
+        load_scales(kb_begin, nx[0], nw[0]);
+        if (kb_begin + 1 < kb_end) load_scales(kb_begin + 1, nx[1], nw[1]);
+        auto add_block = [&](int kb, float (&nx)[SC], float (&nw)[SC]) {
           const uint32_t acc = acc_i & 1u;
           float* sc = my_scale + acc * HC;
 #pragma unroll
           for (int i = 0; i < SC; ++i)
             if (i * 32 + lane < HC) sc[i * 32 + lane] = nx[i] * nw[i];
           __syncwarp();
-          if (kb + 1 < kb_end) load_scales(kb + 1);
-          if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) {
-            ok = false;
-            break;
-          }
+          if (kb + 2 < kb_end) load_scales(kb + 2, nx, nw);
+          if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) return false;
           tc_fence_after();
           const uint32_t base = lane_base + acc * C::COLS;
           // two 8-column groups at a time, the next two on their way
@@ -535,6 +551,12 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
             if (c + 1 < HC / 16) tmem_ld_wait();
             if (c + 2 == HC / 16 || (HC == 16 && c == 0)) release(acc);
           }
+          ++acc_i;
+          return true;
+        };
+        for (int kb = kb_begin; ok && kb < kb_end; kb += 2) {
+          ok = add_block(kb, nx[0], nw[0]);
+          if (ok && kb + 1 < kb_end) ok = add_block(kb + 1, nx[1], nw[1]);
         }
         if (!ok) break;
         if (splits > 1) {
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kGroupedThreads, OCC)
 
   if (CG == 1 && splits > 1) {
     cluster_sync();  // every CTA's sums are there
-    if (warp >= 2 && worker < units.count) {
+    if (warp >= 2 && warp < 10 && worker < units.count) {
       const GroupedTile t = units.get(worker);
       const int quarter = warp & 3, half = (warp - 2) >> 2;
       uint8_t* out = sOut + (warp - 2) * 512;

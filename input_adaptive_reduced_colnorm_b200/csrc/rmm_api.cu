@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1981,8 +1982,8 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
   const dim3 grid(static_cast<unsigned>(workers * CG * splits));
   if (CG == 2 || splits > 1)
-    e = launch_cluster(kern, grid, dim3(kGroupedThreads), smem, static_cast<int>(CG * splits), s, tw, tx, p);
-  else e = launch_chained(kern, grid, dim3(kGroupedThreads), smem, s, tw, tx, p);
+    e = launch_cluster(kern, grid, dim3(grouped_threads(FP8)), smem, static_cast<int>(CG * splits), s, tw, tx, p);
+  else e = launch_chained(kern, grid, dim3(grouped_threads(FP8)), smem, s, tw, tx, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return RMM_OK;
 }
@@ -2006,12 +2007,14 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
   // the kernel moves registers between its warpgroups: never launch it with fewer
   // than the split needs, it would wait for them for good
-  static const int regs = [] {
+  static std::atomic<bool> regs_ok{false};
+  if (!regs_ok.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, grouped_fp8_rows_kernel) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs != GroupedFp8Cfg::LAUNCH_REGS)
-    return fail(RMM_ERR_CUDA, "grouped fp8 kernel compiled to %d registers, not %d", regs, GroupedFp8Cfg::LAUNCH_REGS);
+    if (cudaError_t ea = cudaFuncGetAttributes(&a, grouped_fp8_rows_kernel)) return cuda_fail(ea, "grouped fp8 kernel attributes");
+    if (a.numRegs != GroupedFp8Cfg::LAUNCH_REGS)
+      return fail(RMM_ERR_CUDA, "grouped fp8 kernel compiled to %d registers, not %d", a.numRegs, GroupedFp8Cfg::LAUNCH_REGS);
+    regs_ok.store(true, std::memory_order_relaxed);
+  }
   e = launch_cluster(grouped_fp8_rows_kernel, dim3(static_cast<unsigned>(workers * 2)), dim3(GroupedFp8Cfg::THREADS), smem, 2,
                      s, tw, tx, ty, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
