@@ -1,43 +1,44 @@
 // The e4m3 product with block scales for groups of many rows (see grouped.cuh for
-// the formula and the group bounds): tiles of 256 rows of X x 256 columns of W on
-// CTA pairs, rows on the M side.
+// the formula and the group bounds): tiles of 128 rows of X x 256 columns of W, rows
+// on the M side.
 //
 // Why not swapped as the narrow tiles: every 128-deep block's accumulator passes
-// through the epilogue threads, 128 x 256 fp32 per CTA, while the tensor cores
-// spend 512 cycles on the next one.  With rows of X on the lanes a thread's 128
-// columns share ONE scale (its row's times the weight block's), kept in a
-// register, and tensor memory is read in the 32 x 32-bit shape (128 bytes per
-// cycle and warp scheduler: 256 of the 512 cycles; the 16 x 256-bit shape that the
-// swapped form needs reads half as fast, 546 cycles).  What it costs is a group's
-// last tile, 256 rows however few are left.
+// through the epilogue threads, 128 x 256 fp32, while the tensor cores spend 512
+// cycles on the next one.  With rows of X on the lanes a thread's 128 columns share
+// ONE scale (its row's times the weight block's), kept in a register, and tensor
+// memory is read in the 32 x 32-bit shape (128 bytes per cycle and warp scheduler:
+// 256 of the 512 cycles; the 16 x 256-bit shape that the swapped form needs reads half
+// as fast, 546 cycles).  What it costs is a group's last tile, 128 rows however few
+// are left.  One CTA, not a pair: a pair stages a third less (32 KB a block and CTA
+// against 48), but that is not what bounds it, and its 256-row tiles leave more of a
+// group's last one empty (1024 x 4096 x 14336 of 8 groups: 123 us against 152;
+// 8192 x 4096 x 14336 of 8: 566 against 600; 8192 x 8192 x 8192: 635 against 625).
 //
 // A block's product is issued as two of half the columns with barriers of their
 // own, so that the two epilogue warps of a scheduler work out of step (one loads
 // and waits while the other multiplies); each takes the next block's first columns
 // out of tensor memory before it adds the last ones of this block.
 //
-// 4096 x 4096 x 14336: 242-276 us, 1740-1990 TFLOP/s at 1.5-1.6 GHz (the power cap).
+// 4096 x 4096 x 14336: 250-275 us, 1750-1920 TFLOP/s at 1.5-1.6 GHz (the power cap).
 // Bound by the accumulators' round trip (product, commit, epilogue, hand-back: ~1500
 // cycles on two accumulators of 256 columns, all that tensor memory holds) and the
 // epilogue's steps: ~770 cycles a block where the product takes 512, and ~2500 a tile.
 //
-// Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers (even CTA),
-// one for each product, warps 4-11 epilogue: warp w reads
-// lanes 32 (w % 4) .. + 31 of one of the two products.  The columns of product h
-// are two runs, one from each CTA's half of the tile: [h w / 4, (h + 1) w / 4) and
-// w / 2 further, w the tile's columns.  Results go through 4 KB of shared memory
-// per warp: 32 rows x 64 columns that all belong to the group and the matrix leave as
-// one TMA store, others row by row, 128 bytes at a time.
-// The tiles of a partial last wave are cut along W into 128- or 64-column pieces.
+// Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers, one for each
+// product, warps 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two
+// products.  Results go through 4 KB of shared memory per warp: 32 rows x 64 columns
+// that all belong to the group and the matrix leave as one TMA store, others row by
+// row, 128 bytes at a time.  The tiles of a partial last wave are cut along W into
+// 128- or 64-column pieces.
 #pragma once
 #include "grouped.cuh"
 
 namespace rmm {
 
 struct GroupedFp8Cfg {
-  static constexpr int X_BYTES = 128 * 128;  // this CTA's 128 rows x 128 contraction indices
-  static constexpr int W_BYTES = 128 * 128;  // its 128 of the 256 columns
-  static constexpr int STAGES = 5;
+  static constexpr int X_BYTES = 128 * 128;  // 128 rows x 128 contraction indices
+  static constexpr int W_BYTES = 256 * 128;  // 128 contraction indices x 256 columns, two boxes of 128
+  static constexpr int STAGES = 3;           // (four measured the same)
   static constexpr int OUT_BYTES = 8 * 32 * 128;  // 32 rows x 64 bf16 columns for each epilogue warp
   static constexpr int THREADS = 384;
   // registers per thread at launch, and the split after the set-up: 128 sums and
@@ -109,7 +110,7 @@ struct GroupedFp8Units {
     const int r = tile - pre[lo] * n_tiles;
     t.group = lo;
     t.mtile = (r / rt) * 256 + part * t.w;
-    t.row0 = off[lo] + (r % rt) * 256;
+    t.row0 = off[lo] + (r % rt) * 128;
     t.row_end = off[lo + 1];
     return t;
   }
@@ -126,10 +127,10 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   uint8_t* sX = smem;
   uint8_t* sW = smem + STAGES * C::X_BYTES;
   uint8_t* sOut = sW + STAGES * C::W_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);  // used in the even CTA
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 4;  // used in the even CTA; both [accumulator][half]
+  uint64_t* tempty = tfull + 4;  // both [accumulator][half]
   uint64_t* drain = tempty + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -137,8 +138,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   int* pre = off + p.groups + 1;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues the MMAs
-  const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
+  const int worker = static_cast<int>(blockIdx.x), workers = static_cast<int>(gridDim.x);
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     }
     for (int a = 0; a < 4; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 8);  // four epilogue warps of each CTA
+      mbar_init(&tempty[a], 4);  // four epilogue warps
     }
     mbar_init(drain, 2);
     *abort_flag = 0;
@@ -156,39 +156,37 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     prefetch_tensormap(&tmY);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 512);
-    tmem_relinquish_pair();
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
   }
   wait_prior_kernels();  // bounds, operands and the output are touched only after this
-  grouped_bounds<256>(p, off, pre, warp, lane);
+  grouped_bounds<128>(p, off, pre, warp, lane);
   tc_fence_before();
-  cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
+  __syncthreads();  // barriers initialised, bounds there, tensor memory allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const GroupedFp8Units units(p, off, pre, workers);
 
   if (warp < 4) set_max_regs_down<C::OTHER_REGS>();
   if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
+    // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint32_t full_even = map_shared_rank(smem_u32(&full[0]), 0u);
       int stage = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int unit = worker; ok && unit < units.count; unit += workers) {
         const GroupedTile t = units.get(unit);
-        const int row = t.row0 + static_cast<int>(rank) * 128;
-        const int col = t.mtile + static_cast<int>(rank) * (t.w / 2);
         for (int kb = 0; kb < p.num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (C::X_BYTES + C::W_BYTES));
-          const uint32_t bar = full_even + 8u * static_cast<uint32_t>(stage);
-          tma_load_2d_pair(sX + stage * C::X_BYTES, &tmX, bar, kb * 128, row);
-          // (a narrow piece uses the first t.w / 2 of the 128 columns loaded)
-          tma_load_3d_pair(sW + stage * C::W_BYTES, &tmW, bar, col, kb * 128, t.group);
+          mbar_arrive_expect_tx(&full[stage], C::X_BYTES + C::W_BYTES);
+          uint8_t* w = sW + stage * C::W_BYTES;
+          tma_load_2d(sX + stage * C::X_BYTES, &tmX, &full[stage], kb * 128, t.row0);
+          // (a narrow piece uses the first of the columns loaded)
+          tma_load_3d(w, &tmW, &full[stage], t.mtile, kb * 128, t.group);
+          tma_load_3d(w + 16384, &tmW, &full[stage], t.mtile + 128, kb * 128, t.group);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           }
         }
       }
-      if (!ok && rank == 0) {
+      if (!ok) {
         // wait (bounded) for the stages filled so far, so no copy lands after exit
         for (int s = 0; s < STAGES; ++s) {
           const uint32_t uses = (issued + STAGES - 1 - s) / STAGES;
@@ -210,94 +208,86 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     }
     __syncwarp();
   } else if (warp <= 2) {
-    // ------------------------------------------------------------ MMA issuers (even CTA)
+    // ------------------------------------------------------------ MMA issuers
     // warp 1 issues the product of the first half of the columns, warp 2 that of the
     // second (one warp's waits for both, 3 of about 100 cycles a block, left the
     // tensor cores idle).  The warp runs the loop together and elects the issuing
     // lane, so that the descriptors stay in uniform registers.
-    if (rank == 0) {
-      const int h = warp - 1;
-      const uint64_t xd0 = make_sw128_desc(smem_u32(sX), 16, 1024), wd0 = make_sw128_desc(smem_u32(sW), 16384, 1024);
-      int stage = 0;
-      uint32_t phase = 0, acc_i = 0;
-      bool ok = true;
-      for (int unit = worker; ok && unit < units.count; unit += workers) {
-        const int w = units.get(unit).w;
-        const uint32_t idesc = make_idesc_e4m3(256, 0, 0, 1) | (static_cast<uint32_t>(w >> 4) << 17);  // N = w / 2
-        for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
-          const uint32_t buf = (acc_i & 1u) * 2 + h;
-          const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
-          // w / 4 columns of each CTA
-          const uint64_t wd = wd0 + static_cast<uint64_t>(stage * (C::W_BYTES >> 4)) + static_cast<uint64_t>((h * (w >> 2)) >> 4);
-          // (the operands are there long before the accumulator: asked first, off the
-          // path from one block's epilogue to the next but one's product)
-          const bool go =
-              mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma) &&
-              mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma, 0, kMbarClusterRelaxed);
-          if (!__all_sync(0xffffffffu, go)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_one()) {
+    const int h = warp - 1;
+    const uint64_t xd0 = make_sw128_desc(smem_u32(sX), 16, 1024), wd0 = make_sw128_desc(smem_u32(sW), 16384, 1024);
+    int stage = 0;
+    uint32_t phase = 0, acc_i = 0;
+    bool ok = true;
+    for (int unit = worker; ok && unit < units.count; unit += workers) {
+      const int w = units.get(unit).w;
+      const uint32_t idesc = make_idesc_e4m3(128, 0, 0, 1) | (static_cast<uint32_t>(w >> 4) << 17);  // N = w / 2
+      const int first = w == 256 ? h * 16384 : h * (w >> 1);  // a piece's columns are all in the first box
+      for (int kb = 0; kb < p.num_kb; ++kb, ++acc_i) {
+        const uint32_t buf = (acc_i & 1u) * 2 + h;
+        const uint64_t xd = xd0 + static_cast<uint64_t>(stage * (C::X_BYTES >> 4));
+        const uint64_t wd = wd0 + static_cast<uint64_t>((stage * C::W_BYTES + first) >> 4);
+        // (the operands are there long before the accumulator: asked first, off the
+        // path from one block's epilogue to the next but one's product)
+        const bool go = mbar_wait(&full[stage], phase, abort_flag, kDevErrTimeoutMma) &&
+                        mbar_wait(&tempty[buf], ((acc_i >> 1) & 1u) ^ 1u, abort_flag, kDevErrTimeoutMma);
+        if (!__all_sync(0xffffffffu, go)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_e4m3_pair(tmem_base + buf * 128, xd + static_cast<uint64_t>(kk * (32 >> 4)),
-                             wd + static_cast<uint64_t>(kk * (4096 >> 4)), idesc, kk != 0 ? 1u : 0u);
-            umma_commit_pair(&tfull[buf], 0x3);
-            umma_commit_pair(&empty[stage], 0x3);
-          }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            umma_e4m3(tmem_base + buf * 128, xd + static_cast<uint64_t>(kk * (32 >> 4)),
+                      wd + static_cast<uint64_t>(kk * (4096 >> 4)), idesc, kk != 0 ? 1u : 0u);
+          umma_commit(&tfull[buf]);
+          umma_commit(&empty[stage]);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (elect_one()) {
-        // every MMA issued by this warp is complete once `drain` flips
-        umma_commit_pair(drain, 0x1);
-        const uint32_t a = smem_u32(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
-        }
+    }
+    if (elect_one()) {
+      // every MMA issued by this warp is complete once `drain` flips
+      umma_commit(drain);
+      const uint32_t a = smem_u32(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue (both CTAs)
+    // ------------------------------------------------------------ epilogue
     set_max_regs_up<C::EPI_REGS>();
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tempty_even = map_shared_rank(smem_u32(&tempty[0]), 0u);
     const uint32_t base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
     uint8_t* out = sOut + (warp - 4) * 4096;
     uint32_t acc_i = 0;
     bool ok = true;
-    // the tile at hand; the scales of its next block (s0, s1) and the row's of the two
-    // after; the weight blocks' scales of 32 blocks and of the 32 after, one per lane
-    // (uniform over the warp, they are passed on by shuffles: two loads a block less)
+    // the tile at hand; the scale s of its next block and the row's of the two after;
+    // the weight blocks' scales of 32 blocks and of the 32 after, one per lane (uniform
+    // over the warp, they are passed on by shuffles: a load a block less)
     GroupedTile t;
-    const float *px = nullptr, *pu = nullptr, *pv = nullptr;
-    float s0, s1, x1, x2, u, v, u_next, v_next;
+    const float *px = nullptr, *pw = nullptr;
+    float s, x1, x2, u, u_next;
     auto next_x = [&](int kb) {  // of block kb; past the last one its own again
       const float x = ld_f32_pinned(px);
       px += kb + 1 < p.num_kb ? p.lds : 0;
       return x;
     };
     auto load_w = [&](int kb) {  // of blocks kb .. kb + 31
-      const int64_t at = static_cast<int64_t>(min(kb + lane, p.num_kb - 1)) * p.sw_cols;
-      u_next = ld_f32_pinned(pu + at);
-      v_next = ld_f32_pinned(pv + at);
+      u_next = ld_f32_pinned(pw + static_cast<int64_t>(min(kb + lane, p.num_kb - 1)) * p.sw_cols);
     };
     auto begin = [&](int unit) {
       t = units.get(unit);
-      const int row = t.row0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      const int row = t.row0 + quarter * 32 + lane;
       px = p.sx + (row < t.row_end ? row : 0);
-      // a run of columns lies in one 128-column block of scales (past the edge: any)
-      const float* sw = p.sw + static_cast<int64_t>(t.group) * p.num_kb * p.sw_cols;
-      const int col0 = t.mtile + half * (t.w / 4);
-      pu = sw + min(col0 / 128, p.sw_cols - 1);
-      pv = sw + min((col0 + t.w / 2) / 128, p.sw_cols - 1);
-      s0 = next_x(0);
+      // this warp's columns lie in one 128-column block of scales (past the edge: any)
+      const int block = min((t.mtile + half * (t.w / 2)) / 128, p.sw_cols - 1);
+      pw = p.sw + static_cast<int64_t>(t.group) * p.num_kb * p.sw_cols + block;
+      s = next_x(0);
       x1 = next_x(1);
       x2 = next_x(2);
       load_w(0);
@@ -305,9 +295,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     if (worker < units.count) begin(worker);
     for (int unit = worker; unit < units.count; unit += workers) {
       u = u_next;
-      v = v_next;
-      s1 = s0 * __shfl_sync(0xffffffffu, v, 0);
-      s0 *= __shfl_sync(0xffffffffu, u, 0);
+      s *= __shfl_sync(0xffffffffu, u, 0);
       if (p.num_kb > 32) load_w(32);
       float sum[128];
 #pragma unroll
@@ -322,10 +310,9 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
         ++acc_i;
         if ((kb & 31) == 31) {
           u = u_next;
-          v = v_next;
           if (kb + 33 < p.num_kb) load_w(kb + 33);
         }
-        float s0_next = 0.f, s1_next = 0.f;
+        float s_next = 0.f;
         // 16 columns at a time, the next 16 on their way (a narrow piece reads past
         // its columns, inside the accumulator; those sums are not stored).  The
         // loads stand outside every branch, and the additions keep their place:
@@ -337,8 +324,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           tmem_ld_wait();
           if (c < 7) {
             tmem_ld16(base + acc * 256 + (c + 1) * 16, r[(c + 1) & 1]);
-            if (c == 1) s0_next = x1 * __shfl_sync(0xffffffffu, u, (kb + 1) & 31);
-            if (c == 2) s1_next = x1 * __shfl_sync(0xffffffffu, v, (kb + 1) & 31);
+            if (c == 1) s_next = x1 * __shfl_sync(0xffffffffu, u, (kb + 1) & 31);
             if (c == 3) {
               x1 = x2;
               x2 = next_x(kb + 3);
@@ -346,7 +332,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           } else {
             tc_fence_before();
             __syncwarp();
-            if (elect_one()) mbar_arrive_cluster_relaxed(tempty_even + 8u * (acc * 2 + half));
+            if (elect_one()) mbar_arrive(&tempty[acc * 2 + half]);
             if (kb + 1 < p.num_kb && __any_sync(0xffffffffu, !ready))
               ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
             tc_fence_after();
@@ -354,27 +340,24 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            if (c == 5 && e == 0) ready = test_wait_fma16(smem_u32(next_full), (acc_i >> 1) & 1u, &sum[c * 16], r[c & 1], s1);
-            if (c != 5) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), c < 4 ? s0 : s1);
+            if (c == 5 && e == 0) ready = test_wait_fma16(smem_u32(next_full), (acc_i >> 1) & 1u, &sum[c * 16], r[c & 1], s);
+            if (c != 5) fma_pinned(sum[c * 16 + e], __uint_as_float(r[c & 1][e]), s);
           }
         }
-        s0 = s0_next;
-        s1 = s1_next;
+        s = s_next;
       }
       tmem_ld_wait();
       if (!ok) break;
-      const int run = t.w / 4;                // columns of each of this warp's two runs
-      const int col0 = t.mtile + half * run;  // the first run's; the second starts t.w / 2 further
-      const int skip = t.w / 2 - run;
-      const int row0 = t.row0 + static_cast<int>(rank) * 128 + quarter * 32;
+      const int hw = t.w / 2;                 // this warp's columns: 128, 64 or 32
+      const int col0 = t.mtile + half * hw;
+      const int row0 = t.row0 + quarter * 32;
       const int row_end = t.row_end;
-      const bool whole = t.w == 256 && row0 + 32 <= row_end;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {  // accumulator columns 64 q .. 64 q + 63
+      for (int q = 0; q < 2; ++q) {  // columns 64 q .. 64 q + 63 of them
         if (q == 1) {
           // the next tile's scales come while this one is written
           if (unit + workers < units.count) begin(unit + workers);
-          if (64 >= 2 * run) break;
+          if (hw <= 64) break;
         }
         if (lane == 0) bulk_wait_group_read<0>();  // the last store has left the buffer
         __syncwarp();
@@ -389,8 +372,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           *reinterpret_cast<uint4*>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         // (a store that crosses column m would write zeros up to the next 16 bytes)
-        const int first = col0 + q * (64 + skip);  // where run = 64
-        if (whole && first + 64 <= p.m) {
+        const int first = col0 + q * 64;
+        if (hw >= 64 && row0 + 32 <= row_end && first + 64 <= p.m) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -400,10 +383,9 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
           continue;
         }
         __syncwarp();
-        const int k = lane & 7;              // 8 columns of this thread's rows lane / 8, + 4, ...
-        const int a = q * 64 + k * 8;
-        const int col = col0 + a + (a >= run ? skip : 0);
-        const int left = a < 2 * run ? p.m - col : 0;  // columns that exist
+        const int k = lane & 7;  // 8 columns of this thread's rows lane / 8, + 4, ...
+        const int col = first + k * 8;
+        const int left = q * 64 + k * 8 < hw ? p.m - col : 0;  // columns that exist
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int i = it * 4 + (lane >> 3);
@@ -427,10 +409,10 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   }
 
   tc_fence_before();
-  cluster_sync();  // both CTAs are done with every MMA, copy and accumulator
+  __syncthreads();  // every MMA, copy and accumulator is done with
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, 512);
+    tmem_dealloc(tmem_base, 512);
   }
 }
 

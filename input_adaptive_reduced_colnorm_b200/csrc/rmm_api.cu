@@ -1989,6 +1989,8 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
 }
 
 rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
+  using Cfg = GroupedFp8Cfg;
+  auto kern = grouped_fp8_rows_kernel;
   CUtensorMap tw, tx;
   if (rmm_status st = make_tmaps_grouped(&tw, &tx, true, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx, 128))
     return st;
@@ -1999,24 +2001,23 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   GroupedParams p = c.p;
   p.num_kb = static_cast<int>(ceil_div(c.d, 128));
   p.m_tiles = static_cast<int>(ceil_div(c.m, 256));
-  const int64_t row_tiles = ceil_div(c.n, 256) + std::min<int64_t>(c.groups - 1, c.n);
+  const int64_t row_tiles = ceil_div(c.n, 128) + std::min<int64_t>(c.groups - 1, c.n);
   if (4 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
-  const int64_t workers = std::min<int64_t>(4 * row_tiles * p.m_tiles, std::max(1, num_sms() / 2));
-  const int smem = GroupedFp8Cfg::smem_bytes(static_cast<int>(c.groups));
-  cudaError_t e = cudaFuncSetAttribute(grouped_fp8_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int64_t workers = std::min<int64_t>(4 * row_tiles * p.m_tiles, num_sms());
+  const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
   // the kernel moves registers between its warpgroups: never launch it with fewer
   // than the split needs, it would wait for them for good
   static std::atomic<bool> regs_ok{false};
   if (!regs_ok.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a{};
-    if (cudaError_t ea = cudaFuncGetAttributes(&a, grouped_fp8_rows_kernel)) return cuda_fail(ea, "grouped fp8 kernel attributes");
-    if (a.numRegs != GroupedFp8Cfg::LAUNCH_REGS)
-      return fail(RMM_ERR_CUDA, "grouped fp8 kernel compiled to %d registers, not %d", a.numRegs, GroupedFp8Cfg::LAUNCH_REGS);
+    if (cudaError_t ea = cudaFuncGetAttributes(&a, kern)) return cuda_fail(ea, "grouped fp8 kernel attributes");
+    if (a.numRegs != Cfg::LAUNCH_REGS)
+      return fail(RMM_ERR_CUDA, "grouped fp8 kernel compiled to %d registers, not %d", a.numRegs, Cfg::LAUNCH_REGS);
     regs_ok.store(true, std::memory_order_relaxed);
   }
-  e = launch_cluster(grouped_fp8_rows_kernel, dim3(static_cast<unsigned>(workers * 2)), dim3(GroupedFp8Cfg::THREADS), smem, 2,
-                     s, tw, tx, ty, p);
+  e = launch_chained(kern, dim3(static_cast<unsigned>(workers)), dim3(Cfg::THREADS), smem, s, tw, tx, ty, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return RMM_OK;
 }
@@ -2035,9 +2036,12 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
 //     54 against 59 with 256 columns and 60 with 64 rows, but not for a matrix of one
 //     such tile (1989 x 8330 x 218 of 120: 71 against 49 with 64 rows).
 //   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
-//     83 with 32; e4m3 up to 128 rows: 128 x 4096 x 14336 22 against 23 with 256 rows.
-//   256 x 256 on CTA pairs for more, unless their tiles leave most SMs idle (256 x
-//     4096 x 4096: 24 against 20 with 64 rows; 512 x 4096 x 4096: 25 against 28).
+//     83 with 32; and for more rows where there are few larger tiles (256 x 4096 x 4096:
+//     20 against 24 with 256 rows, e4m3 16 against 19 with 128; 512 x 4096 x 4096, the
+//     other side: 28 against 25, e4m3 20 against 20).
+//   bf16: 256 x 256 on CTA pairs for more.
+//   e4m3: 128 x 256, rows on the lanes, for more (grouped_fp8.cuh): 768 x 4096 x 14336
+//     of 8 103 against 125 with 64 rows, 512 of 8 102 against 100.
 template <bool FP8>
 rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   const int64_t rows = ceil_div(c.n, c.groups);  // of an average group
@@ -2045,7 +2049,8 @@ rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   if (small <= num_sms() && (!FP8 || 2 * small <= num_sms() || c.d <= 2048)) return launch_grouped_t<FP8, 32, 1, 1>(c, s);
   if (rows <= 16) return launch_grouped_t<FP8, 16, 2, 1, 2>(c, s);
   if (rows <= 32 && (!FP8 || c.m > 256)) return launch_grouped_t<FP8, 32, FP8 ? 4 : 2, 1>(c, s);
-  if (rows <= (FP8 ? 128 : 64) || 5 * grouped_tiles(c, 256, 256) < num_sms()) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
+  const bool few = FP8 ? 5 * grouped_tiles(c, 128, 256) < 2 * num_sms() : 5 * grouped_tiles(c, 256, 256) < num_sms();
+  if (rows <= 64 || few) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
   if constexpr (FP8) return launch_grouped_fp8_rows(c, s);
   else return launch_grouped_t<false, 256, 1, 2>(c, s);
 }
