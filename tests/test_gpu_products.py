@@ -209,8 +209,10 @@ TILES = [
     ([3, 0, 16, 1, 17, 9], 300, 4200),                     # 16 rows x 256 columns
     ([30, 1, 33, 32, 0, 16, 40, 31], 200, 2600),           # 32 x 512
     ([64, 70, 0, 1, 63, 40, 65, 64, 50, 60], 264, 2100),   # 64 x 256
-    ([129, 255, 0, 256, 257, 300, 1], 130, 2300),          # 256 x 256, one wave
-    ([1000, 31, 130], 200, 4100),                          # 256 x 256, a last wave of narrow pieces
+    ([129, 255, 0, 256, 257, 300, 1], 130, 2300),          # 256 x 256 (fp8 128 x 256), one wave
+    ([1000, 31, 130], 200, 4100),                          # the same, a last wave of narrow pieces
+    ([128, 127, 100, 1, 129, 64], 1100, 3300),             # fp8 128 x 256, more than 8 blocks
+    ([150, 20, 300], 4300, 2100),                          # more than 32 blocks
     ([1030], 72, 5000),
     ([200, 513, 290], 1000, 5100),
 ]
