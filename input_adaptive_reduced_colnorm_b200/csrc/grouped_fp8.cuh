@@ -20,9 +20,11 @@
 // out of tensor memory before it adds the last ones of this block.
 //
 // 4096 x 4096 x 14336: 250-275 us, 1750-1920 TFLOP/s at 1.5-1.6 GHz (the power cap).
-// Bound by the accumulators' round trip (product, commit, epilogue, hand-back: ~1500
-// cycles on two accumulators of 256 columns, all that tensor memory holds) and the
-// epilogue's steps: ~770 cycles a block where the product takes 512, and ~2500 a tile.
+// ~880 cycles a block, tile changes included, where the product takes 512.  No one
+// thing bounds it: with a quarter of the products 850 are left, without the additions
+// 790, without both 730 -- staging (48 KB a block, 66 bytes a cycle; copies alone reach
+// 77) and the accumulators' round trip (product, commit, epilogue, hand-back) on the two
+// accumulators of 256 columns that tensor memory holds; ~2500 cycles a tile.
 //
 // Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers, one for each
 // product, warps 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two
