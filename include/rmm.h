@@ -266,7 +266,8 @@ rmm_status rmm_linear_int8(const rmm_bf16* A, int64_t n, int64_t d, int64_t lda,
  *   a = max |X[i, 128 b : 128 b + 128]|,  sx[b][i] = fl(a / 448), or 1 if that is 0,
  *   Xq[i, j] = e4m3(fl(X[i, j] / sx[b][i])),
  * both divisions IEEE fp32, e4m3 to nearest even.  A block that holds a NaN has
- * a NaN scale; one that holds an infinity has an infinite one.
+ * a NaN scale; one that holds an infinity has an infinite one.  The sign of a
+ * zero among X is not kept.
  *   X   device bf16 [n][ldx], ldx >= d, a multiple of 8.
  *   Xq  device e4m3 [n][ldq], ldq >= d, a multiple of 16 (columns past d are not written).
  *   sx  device fp32 [ceil(d / 128)][lds], lds >= n: a block's scales side by side.
@@ -288,7 +289,7 @@ rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_
  *   Wq      device e4m3 [d][ldw], ldw >= m, a multiple of 16 (contraction index as the row).
  *   sw      device fp32 [ceil(d / 128)][ceil(m / 128)].
  *   Y       device bf16 [n][ldy].
- * n = 0 is valid and does nothing.  Limits: n, d, m < 2^31 - 512.  No workspace. */
+ * n = 0 is valid and does nothing.  Limits: d <= 2^24; n, m < 2^31 - 512.  No workspace. */
 rmm_status rmm_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
                           const rmm_e4m3* Wq, int64_t m, int64_t ldw, const float* sw, rmm_bf16* Y, int64_t ldy,
                           rmm_stream stream);
@@ -308,7 +309,7 @@ rmm_status rmm_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx,
  *   Y        device bf16 [n][ldy]; rows before offsets[0] and from offsets[groups]
  *            on are left as they were.
  * The rows a tile takes go by n / groups: uneven groups are right, only slower.
- * n = 0 is valid and does nothing.  Limits: groups <= 1024; n, d, m < 2^31 - 512.
+ * n = 0 is valid and does nothing.  Limits: groups <= 1024; d <= 2^24; n, m < 2^31 - 512.
  * No workspace. */
 rmm_status rmm_grouped_linear(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, const rmm_bf16* W, int64_t groups,
                               int64_t w_stride, int64_t m, int64_t ldw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy,

@@ -1978,7 +1978,9 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   const int64_t workers = splits > 1 ? row_tiles * p.m_tiles : std::min<int64_t>((N >= 128 ? N / 32 : 1) * row_tiles * p.m_tiles, std::max(1, num_sms() * OCC / CG));
   const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
   auto kern = grouped_kernel<FP8, N, MT, CG, OCC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit for the most groups, whatever the call has: with its own, a call of another
+  // thread with more groups, between here and its launch, would be refused
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem_bytes(kGroupedMaxGroups));
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
   const dim3 grid(static_cast<unsigned>(workers * CG * splits));
   if (CG == 2 || splits > 1)
@@ -2005,7 +2007,8 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   if (4 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
   const int64_t workers = std::min<int64_t>(4 * row_tiles * p.m_tiles, num_sms());
   const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (for the most groups, as above)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem_bytes(kGroupedMaxGroups));
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
   // the kernel moves registers between its warpgroups: never launch it with fewer
   // than the split needs, it would wait for them for good
@@ -2062,7 +2065,9 @@ rmm_status check_product(const void* X, int64_t n, int64_t d, int64_t ldx, const
     return fail(RMM_ERR_INVALID_ARG, "n must be >= 0; d, m and groups must be >= 1");
   if (W == nullptr || (n > 0 && (X == nullptr || Y == nullptr))) return fail(RMM_ERR_INVALID_ARG, "X, W and Y are required");
   if (ldx < d || ldw < m || ldy < m) return fail(RMM_ERR_INVALID_ARG, "leading dimension too small");
-  if (n > kIntMax - 256 || d > kIntMax - 256 || m > kIntMax - 512 || ldx > (1LL << 36) || ldw > (1LL << 36) ||
+  // (d: a bf16 tile's epilogue waits for its whole contraction, at most 2^18 stages of about 1 us with every
+  // SM loading, well inside the waits' limit of a second)
+  if (n > kIntMax - 256 || d > (1LL << 24) || m > kIntMax - 512 || ldx > (1LL << 36) || ldw > (1LL << 36) ||
       ldy > (1LL << 36) || d * ldw > (1LL << 38))
     return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
   if (groups > kGroupedMaxGroups) return fail(RMM_ERR_UNSUPPORTED, "at most %d groups", kGroupedMaxGroups);

@@ -547,3 +547,42 @@ def test_two_streams_at_once():
             got.append((rmm.grouped_linear(X[:200], W, off), b))
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in got)
+
+
+@pytest.mark.parametrize("rows,d,m", [(6, 128, 6400), (256, 128, 2560)])
+def test_threads_with_other_group_counts(rows, d, m):
+    """Host threads whose calls have few and many groups (whose bounds take more of a
+    kernel's shared memory) at once: none is refused, each result is that of a call alone."""
+    import threading
+
+    g = torch.Generator(device="cuda").manual_seed(76)
+    calls = []
+    for E in (3, 300):
+        n = rows * E
+        X = torch.randn((n, d), generator=g, device="cuda").bfloat16()
+        W = torch.randn((E, d, m), generator=g, device="cuda").bfloat16()
+        off = torch.arange(0, n + 1, rows, dtype=torch.int32, device="cuda")
+        args = (*rmm.quantize_fp8(X), *rmm.quantize_fp8_weight(W), off)
+        calls += [(rmm.grouped_linear, (X, W, off)), (rmm.grouped_linear_fp8, args)]
+    alone = [f(*a) for f, a in calls]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        f, a = calls[i]
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                out = torch.empty_like(alone[i])
+                for _ in range(100):
+                    f(*a, out=out)
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(out, alone[i])
+        except Exception as e:  # noqa: BLE001
+            failed.append((i, e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed

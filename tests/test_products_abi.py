@@ -147,3 +147,12 @@ def test_oracle_grouped_by_hand():
     W = [np.eye(2), 2 * np.eye(2), 3 * np.eye(2)]
     Y = oracle.grouped_product(X, W, [1, 1, 3, 2], np.full((4, 2), 9.0))
     assert Y.tolist() == [[9, 9], [4, 6], [8, 10], [9, 9]]  # group 0 empty, group 2's end clamped to its start
+
+
+def test_contraction_limit(L):
+    """A contraction past 2^24 would keep a tile's epilogue waiting for most of the limit of its waits."""
+    d = 1 << 24
+    f = lambda d: L.rmm_linear_fp8(P16, 0, d, 1 << 25, P16, 1, P16, 16, 16, P16, P16, 16, None)  # noqa: E731
+    g = lambda d: L.rmm_grouped_linear(P16, 0, d, 1 << 25, P16, 2, 1 << 30, 16, 16, P16, P16, 16, None)  # noqa: E731
+    assert f(d) == OK and g(d) == OK
+    assert f(d + 1) == UNSUPPORTED and g(d + 1) == UNSUPPORTED
