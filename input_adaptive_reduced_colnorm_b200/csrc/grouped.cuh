@@ -30,7 +30,8 @@
 // 512 at 1.3-1.45 GHz).
 //
 // Tiles are cut to the rows that are there: the N of a tile's instructions is
-// its row count rounded up to 16 (32 for a pair).  When the tiles do not fill a
+// its row count rounded up to 16 (32 for a pair), and one CTA copies only the runs of
+// 32 rows that hold some.  When the tiles do not fill a
 // whole number of waves, those of the last wave are cut into narrower ones.
 //
 // Few tiles (decoding): the contraction of a tile is split over the 2 to 8 CTAs of
@@ -42,8 +43,11 @@
 // clamps them to 0 <= ... <= n, non-decreasing, and sums the row tiles of the
 // groups before it starts; a tile number is looked up by bisection.
 //
-// Roles (320 threads, e4m3 352): warp 0 TMA producer, warp 1 (and for e4m3 warp 10)
-// MMA issuer, warps 2-9 epilogue.  CG = 2: two CTAs of a cluster form one M = 256
+// Roles: warp 0 TMA producer, warp 1 (and for e4m3 the last warp) MMA issuer, warps from
+// 2 on epilogue: 8, and 16 for the e4m3 tiles of 128 accumulator columns, whose every
+// block goes through them (64 x 4096 x 14336: 16.5 us against 20.1 with 8; 4096 x 2048 x
+// 1408 of 64 groups 46 against 48; each waits for its loads of tensor memory, and two
+// warps a scheduler do not cover that).  CG = 2: two CTAs of a cluster form one M = 256
 // product (256 columns of W x 256 rows of X), each staging its own 128 columns of W
 // and half of the rows.
 #pragma once
@@ -53,7 +57,6 @@
 namespace rmm {
 
 constexpr int kGroupedMaxGroups = 1024;
-constexpr int grouped_threads(bool fp8) { return fp8 ? 352 : 320; }
 
 struct GroupedParams {
   const int32_t* offsets;  // [groups + 1] on the device, or null: one group of n rows
@@ -71,16 +74,19 @@ struct GroupedParams {
   int sw_cols;
 };
 
-template <int N, int MT, int CG, int OCC>
+template <bool FP8, int N, int MT, int CG, int OCC>
 struct GroupedCfg {
   static constexpr int A_BYTES = MT * 128 * 128;
   static constexpr int X_ROWS = N / CG;
   static constexpr int X_BYTES = X_ROWS * 128;
+  static constexpr int X_BOX = CG == 1 && X_ROWS > 32 ? 32 : X_ROWS;  // rows of a copy
   static constexpr int COLS = MT * N;          // accumulator columns of one tile
-  static constexpr int HC = COLS / 2;          // columns of one epilogue thread
+  static constexpr int EW = FP8 && COLS >= 128 ? 16 : 8;  // epilogue warps
+  static constexpr int THREADS = (2 + EW + (FP8 ? 1 : 0)) * 32;
+  static constexpr int HC = COLS / (EW / 4);   // columns of one epilogue thread
   static constexpr int TMEM_COLS = 2 * COLS;
-  static constexpr int SCALE_BYTES = 8 * 2 * HC * 4;
-  static constexpr int OUT_BYTES = 8 * 512;    // results on their way, 512 bytes per epilogue warp
+  static constexpr int SCALE_BYTES = FP8 ? EW * 2 * HC * 4 : 0;
+  static constexpr int OUT_BYTES = EW * 512;   // results on their way, 512 bytes per epilogue warp
   // OCC CTAs share an SM (with the bounds of up to 128 groups; more lower it to one)
   static constexpr int BOUND_GROUPS = OCC == 1 ? kGroupedMaxGroups : 128;
   static constexpr int STAGES_FIT =
@@ -250,12 +256,23 @@ __device__ __forceinline__ void grouped_store(const GroupedParams& p, uint8_t* b
   }
 }
 
+// Row of the tile and 128-column tile of W of accumulator column share * HC + i (one
+// of HC and N is a multiple of the other).
+template <int N, int HC>
+__device__ __forceinline__ int grouped_r(int share, int i) {
+  return HC >= N ? i % N : share % (N / HC > 0 ? N / HC : 1) * HC + i;
+}
+template <int N, int HC>
+__device__ __forceinline__ int grouped_mt(int share, int i) {
+  return HC >= N ? share * (HC / N) + i / N : share / (N / HC > 0 ? N / HC : 1);
+}
+
 template <bool FP8, int N, int MT, int CG, int OCC>
-__global__ void __launch_bounds__(grouped_threads(FP8), OCC)
+__global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const GroupedParams p) {
-  using C = GroupedCfg<N, MT, CG, OCC>;
-  constexpr int STAGES = C::STAGES, HC = C::HC;
+  using C = GroupedCfg<FP8, N, MT, CG, OCC>;
+  constexpr int STAGES = C::STAGES, HC = C::HC, EW = C::EW;
   constexpr int BK = FP8 ? 128 : 64;
   // the instructions' N is set per tile
   constexpr uint32_t IDESC0 = FP8 ? make_idesc_e4m3(128 * CG, 0, 1, 0) : make_idesc_bf16(128 * CG, 0, 1, 0);
@@ -266,7 +283,7 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(grouped_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sX = smem + STAGES * C::A_BYTES;
-  float* sScale = reinterpret_cast<float*>(sX + STAGES * C::X_BYTES);  // [8 warps][2][HC]
+  float* sScale = reinterpret_cast<float*>(sX + STAGES * C::X_BYTES);  // [EW warps][2][HC]
   uint8_t* sOut = reinterpret_cast<uint8_t*>(sScale) + C::SCALE_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);  // even CTA
   uint64_t* empty = full + STAGES;
@@ -293,7 +310,7 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 8 * CG);
+      mbar_init(&tempty[a], EW * CG);
     }
     mbar_init(drain, FP8 ? 2 : 1);
     *abort_flag = 0;
@@ -331,12 +348,13 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
         if (t.w == 0) continue;
         const int f0 = (t.mtile * CG + static_cast<int>(rank)) * MT * 128;
         const int row = t.row0 + static_cast<int>(rank) * (t.w / 2);  // half of a pair's rows
+        const int x_boxes = CG == 2 ? 1 : (t.w + C::X_BOX - 1) / C::X_BOX;  // those that hold rows of the tile
         for (int kb = kb_begin; kb < kb_end; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * (C::A_BYTES + C::X_BYTES));
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * (C::A_BYTES + x_boxes * C::X_BOX * 128));
           uint8_t* a = sA + stage * C::A_BYTES;
           uint8_t* x = sX + stage * C::X_BYTES;
           constexpr int BOXES = FP8 ? MT : 2 * MT;     // boxes of 128 bytes of columns
@@ -351,7 +369,8 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
 #pragma unroll
             for (int j = 0; j < BOXES; ++j)
               tma_load_3d(a + j * (BK * 128), &tmW, &full[stage], f0 + j * BOX_COLS, kb * BK, t.group);
-            tma_load_2d(x, &tmX, &full[stage], kb * BK, row);
+            for (int j = 0; j < x_boxes; ++j)
+              tma_load_2d(x + j * (C::X_BOX * 128), &tmX, &full[stage], kb * BK, row + j * C::X_BOX);
           }
           ++issued;
           if (++stage == STAGES) {
@@ -373,9 +392,9 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 10) {
+  } else if (warp == 1 || warp == 2 + EW) {
     // ------------------------------------------------------------ MMA issuers (even CTA)
-    // e4m3: warp 1 issues the even blocks' products, warp 10 the odd ones', each to an
+    // e4m3: warp 1 issues the even blocks' products, the last warp the odd ones', each to an
     // accumulator of its own.  Issuing takes about as long as the products, and one
     // warp's waits between them (accumulator, operands: 400 cycles a block) would leave
     // the tensor cores idle.  bf16 adds to one accumulator and waits once a tile.
@@ -468,12 +487,12 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3;         // lanes of tensor memory a warp may read
-    const int half = (warp - 2) >> 2;
-    // this thread's accumulator columns [half * HC, half * HC + HC): rows r_of(i)
+    const int share = (warp - 2) >> 2;
+    // this thread's accumulator columns [share * HC, share * HC + HC): rows r_of(i)
     // of the tile, columns of W in its 128-column tile mt_of(i)
-    auto mt_of = [&](int i) { return HC >= N ? half * (HC / N) + i / N : 0; };
-    auto r_of = [&](int i) { return HC >= N ? i % N : half * HC + i; };
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HC);
+    auto mt_of = [&](int i) { return grouped_mt<N, HC>(share, i); };
+    auto r_of = [&](int i) { return grouped_r<N, HC>(share, i); };
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(share * HC);
     const uint32_t tempty_even = CG == 2 ? map_shared_rank(smem_u32(&tempty[0]), 0u) : 0u;
     float* my_scale = sScale + (warp - 2) * 2 * HC;
     uint8_t* out = sOut + (warp - 2) * 512;
@@ -600,9 +619,9 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
 
   if (CG == 1 && splits > 1) {
     cluster_sync();  // every CTA's sums are there
-    if (warp >= 2 && warp < 10 && worker < units.count) {
+    if (warp >= 2 && warp < 2 + EW && worker < units.count) {
       const GroupedTile t = units.get(worker);
-      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      const int quarter = warp & 3, share = (warp - 2) >> 2;
       uint8_t* out = sOut + (warp - 2) * 512;
       const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((((warp - 2) * (HC / 2)) * 32 + lane) * 8);
 #pragma unroll
@@ -621,10 +640,8 @@ __global__ void __launch_bounds__(grouped_threads(FP8), OCC)
         uint64_t v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = pack_u64(__float_as_uint(s[j].x), __float_as_uint(s[j].y));
-        const int i = g * 8;
-        const int mt = HC >= N ? half * (HC / N) + i / N : 0;
-        const int row = HC >= N ? i % N : half * HC + i;
-        grouped_store(p, out, v, t.row0 + row, t.row_end, (t.mtile * MT + mt) * 128 + quarter * 32, lane);
+        grouped_store(p, out, v, t.row0 + grouped_r<N, HC>(share, g * 8), t.row_end,
+                      (t.mtile * MT + grouped_mt<N, HC>(share, g * 8)) * 128 + quarter * 32, lane);
       }
     }
   }

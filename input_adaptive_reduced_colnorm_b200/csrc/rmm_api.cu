@@ -1949,10 +1949,10 @@ int64_t grouped_tiles(const GroupedCall& c, int64_t rows, int64_t cols) {
 
 template <bool FP8, int N, int MT, int CG, int OCC = 1>
 rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
-  using Cfg = GroupedCfg<N, MT, CG, OCC>;
+  using Cfg = GroupedCfg<FP8, N, MT, CG, OCC>;
   CUtensorMap tw, tx;
   if (rmm_status st = make_tmaps_grouped(&tw, &tx, FP8, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx,
-                                         Cfg::X_ROWS))
+                                         Cfg::X_BOX))
     return st;
   GroupedParams p = c.p;
   p.num_kb = static_cast<int>(ceil_div(c.d, FP8 ? 128 : 64));
@@ -1984,8 +1984,8 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return cuda_fail(e, "grouped product attribute");
   const dim3 grid(static_cast<unsigned>(workers * CG * splits));
   if (CG == 2 || splits > 1)
-    e = launch_cluster(kern, grid, dim3(grouped_threads(FP8)), smem, static_cast<int>(CG * splits), s, tw, tx, p);
-  else e = launch_chained(kern, grid, dim3(grouped_threads(FP8)), smem, s, tw, tx, p);
+    e = launch_cluster(kern, grid, dim3(Cfg::THREADS), smem, static_cast<int>(CG * splits), s, tw, tx, p);
+  else e = launch_chained(kern, grid, dim3(Cfg::THREADS), smem, s, tw, tx, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped product launch");
   return RMM_OK;
 }
