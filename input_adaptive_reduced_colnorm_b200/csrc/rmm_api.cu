@@ -2038,6 +2038,12 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
 //     64 rows, or 512 columns; e4m3 32 x 512, whose blocks are half as long to load:
 //     54 against 59 with 256 columns and 60 with 64 rows, but not for a matrix of one
 //     such tile (1989 x 8330 x 218 of 120: 71 against 49 with 64 rows).
+//     Up to 40 rows where columns past the edge weigh little (2600 x 2048 x 1408 of 64:
+//     43 against 46 with 64 rows; 47 rows a group, 3000 x 1024 x 1408 of 64: 28 against 25).
+//   bf16 128 x 256 for 41 to 64 rows, which leave many groups a second tile of 64, where
+//     such tiles fill three quarters of their waves (2600 x 2048 x 1408 of 64: 64 against
+//     70 with 64 rows, 2000 x 2048 x 2048 of 32 48 against 53, 512 x 4096 x 14336 of 8 157
+//     against 169; 3000 x 4096 x 1024 of 48, 192 tiles: 79 against 68).
 //   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
 //     83 with 32; and for more rows where there are few larger tiles (256 x 4096 x 4096:
 //     20 against 24 with 256 rows, e4m3 16 against 19 with 128; 512 x 4096 x 4096, the
@@ -2051,8 +2057,12 @@ rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   const int64_t small = grouped_tiles(c, 32, 128);
   if (small <= num_sms() && (!FP8 || 2 * small <= num_sms() || c.d <= 2048)) return launch_grouped_t<FP8, 32, 1, 1>(c, s);
   if (rows <= 16) return launch_grouped_t<FP8, 16, 2, 1, 2>(c, s);
-  if (rows <= 32 && (!FP8 || c.m > 256)) return launch_grouped_t<FP8, 32, FP8 ? 4 : 2, 1>(c, s);
+  if (rows <= (FP8 && c.m >= 1024 ? 40 : 32) && (!FP8 || c.m > 256)) return launch_grouped_t<FP8, 32, FP8 ? 4 : 2, 1>(c, s);
   const bool few = FP8 ? 5 * grouped_tiles(c, 128, 256) < 2 * num_sms() : 5 * grouped_tiles(c, 256, 256) < num_sms();
+  const int64_t tiles = grouped_tiles(c, 128, 256), waves = ceil_div(tiles, num_sms());
+  if constexpr (!FP8) {
+    if (!few && rows > 40 && rows <= 64 && 4 * tiles >= 3 * waves * num_sms()) return launch_grouped_t<FP8, 128, 2, 1>(c, s);
+  }
   if (rows <= 64 || few) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
   if constexpr (FP8) return launch_grouped_fp8_rows(c, s);
   else return launch_grouped_t<false, 256, 1, 2>(c, s);

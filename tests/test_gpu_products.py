@@ -528,6 +528,22 @@ def test_large_tiles_captured(fp8):
     del graph
 
 
+# (rows of the groups, d, m) of tiles of 128 x 256 in bf16 (41 to 64 rows an average group,
+# tiles that about fill a wave) and 32 x 512 in e4m3 with more than 32 rows a group
+MEDIUM = [
+    ([128, 60, 0, 1, 33, 31, 100, 64, 17, 16], 200, 3500),   # 140 tiles of 128 x 256
+    ([300, 1, 0, 129, 40, 2, 8, 65, 20, 10, 31, 32], 330, 2900),  # 144, a group of three row tiles
+    ([62, 0, 90, 33, 1, 47], 136, 6100),                     # e4m3 32 x 512
+    ([40, 33, 38, 0, 70, 32, 39, 36], 260, 2100),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("sizes,d,m", MEDIUM, ids=str)
+def test_medium_groups(sizes, d, m, fp8):
+    test_every_tile_shape(sizes, d, m, fp8)
+
+
 def test_two_streams_at_once():
     """Calls on two streams share nothing: interleaved results equal those of calls alone."""
     dev, _, _ = fp8_operands(67, 200, 512, 1024, 4)
