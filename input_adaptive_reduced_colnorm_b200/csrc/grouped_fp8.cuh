@@ -172,39 +172,40 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   if (warp < 4) set_max_regs_down<C::OTHER_REGS>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0;
-      bool ok = true;
-      for (int unit = worker; ok && unit < units.count; unit += workers) {
-        const GroupedTile t = units.get(unit);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[stage], C::X_BYTES + C::W_BYTES);
+    // (elected lane of a warp that runs the loop together, as below)
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int unit = worker; ok && unit < units.count; unit += workers) {
+      const GroupedTile t = units.get(unit);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer))) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          // (a narrow piece's columns are all in the first box of W)
+          mbar_arrive_expect_tx(&full[stage], C::X_BYTES + (t.w == 256 ? C::W_BYTES : C::W_BYTES / 2));
           uint8_t* w = sW + stage * C::W_BYTES;
           tma_load_2d(sX + stage * C::X_BYTES, &tmX, &full[stage], kb * 128, t.row0);
-          // (a narrow piece uses the first of the columns loaded)
           tma_load_3d(w, &tmW, &full[stage], t.mtile, kb * 128, t.group);
-          tma_load_3d(w + 16384, &tmW, &full[stage], t.mtile + 128, kb * 128, t.group);
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (t.w == 256) tma_load_3d(w + 16384, &tmW, &full[stage], t.mtile + 128, kb * 128, t.group);
+        }
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {
-        // wait (bounded) for the stages filled so far, so no copy lands after exit
-        for (int s = 0; s < STAGES; ++s) {
-          const uint32_t uses = (issued + STAGES - 1 - s) / STAGES;
-          if (uses == 0) continue;
-          const uint32_t a = smem_u32(&full[s]);
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(a, (uses - 1) & 1u) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
-          }
+    }
+    if (!ok) {
+      // wait (bounded) for the stages filled so far, so no copy lands after exit
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t uses = (issued + STAGES - 1 - s) / STAGES;
+        if (uses == 0) continue;
+        const uint32_t a = smem_u32(&full[s]);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(a, (uses - 1) & 1u) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
         }
       }
     }
