@@ -26,7 +26,7 @@
 //
 // Bound by HBM with few rows (bf16 64 x 4096 x 14336 of 8 groups: 139 us, the copy
 // bandwidth; e4m3 8 x 8192 x 28672: 39 us, 0.92 of it) and by the tensor cores at the
-// power cap with many (8192 x 4096 x 14336 of 8: 685-855 us, 530 cycles a stage of
+// power cap with many (8192 x 4096 x 14336 of 8: 685-869 us, 530 cycles a stage of
 // 512 at 1.3-1.45 GHz).
 //
 // Tiles are cut to the rows that are there: the N of a tile's instructions is
