@@ -276,7 +276,8 @@ rmm_status rmm_linear_int8(const rmm_bf16* A, int64_t n, int64_t d, int64_t lda,
  *   W   device bf16 [groups][d][ldw], Wq device e4m3 [groups][d][ldq].
  *   sw  device fp32 [groups][ceil(d / 128)][ceil(m / 128)], contiguous.
  * n = 0 is valid and does nothing.  Limits: d <= 2^24 (activations), fewer than
- * 2^31 blocks.  No workspace. */
+ * 2^31 blocks.  No workspace.  These calls and the products below do not work in
+ * place: an output shares no memory with an input. */
 rmm_status rmm_quantize_fp8(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, rmm_e4m3* Xq, int64_t ldq, float* sx,
                             int64_t lds, rmm_stream stream);
 rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_stride, int64_t d, int64_t m, int64_t ldw,

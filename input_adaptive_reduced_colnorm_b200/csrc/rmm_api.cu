@@ -2068,6 +2068,8 @@ rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
   else return launch_grouped_t<false, 256, 1, 2>(c, s);
 }
 
+constexpr const char* kInPlace = "Y must not be X or W: tiles read them while others write Y";
+
 // Checks shared by the product calls; `unit` = elements of 16 bytes.
 rmm_status check_product(const void* X, int64_t n, int64_t d, int64_t ldx, const void* W, int64_t groups,
                          int64_t w_stride, int64_t m, int64_t ldw, const void* Y, int64_t ldy, int64_t unit) {
@@ -2104,6 +2106,7 @@ rmm_status fp8_product(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, co
   if (rmm_status st = check_product(Xq, n, d, ldx, Wq, groups, w_stride, m, ldw, Y, ldy, 16)) return st;
   if (rmm_status st = check_scales(sx, lds, n, sw)) return st;
   if (n == 0) return RMM_OK;
+  if (static_cast<const void*>(Y) == Xq || static_cast<const void*>(Y) == Wq) return fail(RMM_ERR_INVALID_ARG, kInPlace);
   GroupedCall c{};
   c.X = Xq;
   c.n = n;
@@ -2142,6 +2145,7 @@ rmm_status rmm_quantize_fp8(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx
   if (n > kIntMax - 256 || d > (1LL << 24) || ldx > (1LL << 36) || ldq > (1LL << 36))
     return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
   if (n == 0) return RMM_OK;
+  if (static_cast<const void*>(Xq) == X) return fail(RMM_ERR_INVALID_ARG, "Xq must not be X: its rows are written while X is read");
   QuantParams p{};
   p.x = X;
   p.ldx = ldx;
@@ -2185,6 +2189,7 @@ rmm_status rmm_quantize_fp8_weight(const rmm_bf16* W, int64_t groups, int64_t w_
   const int64_t db = ceil_div(d, 128), mb = ceil_div(m, 128);
   if (groups > kIntMax || groups * db > kIntMax || groups * db * mb > kIntMax)
     return fail(RMM_ERR_UNSUPPORTED, "too many blocks");
+  if (static_cast<const void*>(Wq) == W) return fail(RMM_ERR_INVALID_ARG, "Wq must not be W: its rows are written while W is read");
   QuantParams p{};
   p.x = W;
   p.ldx = ldw;
@@ -2218,6 +2223,7 @@ rmm_status rmm_grouped_linear(const rmm_bf16* X, int64_t n, int64_t d, int64_t l
   if (offsets == nullptr) return fail(RMM_ERR_INVALID_ARG, "offsets are required");
   if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
   if (n == 0) return RMM_OK;
+  if (Y == X || Y == W) return fail(RMM_ERR_INVALID_ARG, kInPlace);
   GroupedCall c{};
   c.X = X;
   c.n = n;

@@ -156,3 +156,17 @@ def test_contraction_limit(L):
     g = lambda d: L.rmm_grouped_linear(P16, 0, d, 1 << 25, P16, 2, 1 << 30, 16, 16, P16, P16, 16, None)  # noqa: E731
     assert f(d) == OK and g(d) == OK
     assert f(d + 1) == UNSUPPORTED and g(d + 1) == UNSUPPORTED
+
+
+def test_in_place_is_refused(L):
+    """An output that is an input: refused before anything is enqueued."""
+    P2 = 0x20000
+    assert L.rmm_quantize_fp8(P16, 4, 256, 256, P16, 512, P2, 4, None) == INVALID
+    assert b"Xq must not be X" in L.rmm_last_error()
+    assert L.rmm_quantize_fp8_weight(P16, 1, 0, 256, 256, 256, P16, 0, 512, P2, None) == INVALID
+    assert b"Wq must not be W" in L.rmm_last_error()
+    for X, W, Y in ((P16, P2, P16), (P2, P16, P16)):
+        assert L.rmm_linear_fp8(X, 8, 256, 256, P2, 8, W, 512, 512, P2, Y, 512, None) == INVALID
+        assert b"Y must not be X or W" in L.rmm_last_error()
+        assert L.rmm_grouped_linear(X, 8, 256, 256, W, 2, 1 << 20, 512, 512, P2, Y, 512, None) == INVALID
+        assert b"Y must not be X or W" in L.rmm_last_error()
