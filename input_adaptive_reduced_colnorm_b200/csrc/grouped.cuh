@@ -26,7 +26,7 @@
 //
 // Bound by HBM with few rows (bf16 64 x 4096 x 14336 of 8 groups: 139 us, the copy
 // bandwidth; e4m3 8 x 8192 x 28672: 39 us, 0.92 of it) and by the tensor cores at the
-// power cap with many (8192 x 4096 x 14336 of 8: 685-869 us, 530 cycles a stage of
+// power cap with many (8192 x 4096 x 14336 of 8: 685-890 us, 530 cycles a stage of
 // 512 at 1.3-1.45 GHz).
 //
 // Tiles are cut to the rows that are there: the N of a tile's instructions is
@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
     // ------------------------------------------------------------ producer (both CTAs)
     // (the warp runs the loop together and elects the lane that issues, as the MMA
     // issuers do: the copies' operands then stay in uniform registers; bf16 1 x 4096 x
-    // 14336 30 us against 35 with one lane in the loop, 1024 x 4096 x 14336 of 8 166 against 172)
+    // 14336 30 us against 35 with one lane in the loop, 1024 x 4096 x 14336 of 8 166 against 172;
+    // 8192 x 4096 x 14336 of 8, at the power cap for seconds, 885 against 860)
     const uint32_t full_even = CG == 2 ? map_shared_rank(smem_u32(&full[0]), 0u) : 0u;
     int stage = 0;
     uint32_t phase = 0, issued = 0;

@@ -19,7 +19,7 @@
 // and waits while the other multiplies); each takes the next block's first columns
 // out of tensor memory before it adds the last ones of this block.
 //
-// 4096 x 4096 x 14336: 244-283 us, 1700-1970 TFLOP/s at 1.5-1.6 GHz (the power cap).
+// 4096 x 4096 x 14336: 244-288 us, 1670-1970 TFLOP/s at 1.5-1.6 GHz (the power cap).
 // ~880 cycles a block, tile changes included, where the product takes 512.  No one
 // thing bounds it: with a quarter of the products 850 are left, without the additions
 // 790, without both 730 -- staging (48 KB a block, 66 bytes a cycle; copies alone reach
