@@ -394,8 +394,8 @@ rmm_status rmm_device_error(int32_t* code_out);
 const char* rmm_version(void);
 
 /* ---------------------------------------------------------------- test hooks
- * Two entry points that exist only so that tests can reach device code no
- * product call exposes on its own; neither is part of the method.
+ * Entry points that exist only so that tests can reach device code no product
+ * call exposes on its own, or see which a call takes; none is part of the method.
  *
  * rmm_debug_exp2_poly: y_poly[i] = the fused attention's FMA-pipe 2^x (x split
  * into its nearest integer n and f in [-1/2, 1/2], a cubic fitted to 2^f, the
@@ -417,6 +417,14 @@ rmm_status rmm_debug_exp2_poly(const float* x, float* y_poly, float* y_exp2f, in
 rmm_status rmm_debug_gemm_expire_producer(const rmm_bf16* A_pack, int64_t n, int64_t k, int64_t lda,
                                           const rmm_bf16* B_pack, int64_t m, int64_t ldb, rmm_bf16* Y, int64_t ldy,
                                           rmm_stream stream);
+
+/* rmm_debug_grouped_plan: how rmm_grouped_linear (e4m3 = 0) or
+ * rmm_grouped_linear_fp8 (1; rmm_linear_fp8 with groups = 1) tiles a call on a GPU
+ * of `sms` SMs: plan_out[0] rows of X and plan_out[1] columns of W of a tile,
+ * plan_out[2] CTAs that share one's contraction.  Host only: no device is touched;
+ * plan_out is host memory. */
+rmm_status rmm_debug_grouped_plan(int e4m3, int64_t n, int64_t d, int64_t m, int64_t groups, int32_t sms,
+                                  int32_t* plan_out);
 
 #ifdef __cplusplus
 }

@@ -1941,14 +1941,80 @@ struct GroupedCall {
   GroupedParams p;
 };
 
-// Tiles of `rows` rows x `cols` columns that a call is taken to have: its groups as
-// even as they can be, one tile at least for each (the bounds are on the device).
-int64_t grouped_tiles(const GroupedCall& c, int64_t rows, int64_t cols) {
-  return std::max(ceil_div(c.n, rows), std::min(c.groups, c.n)) * ceil_div(c.m, cols);
+// How the products of a call are tiled: rows of X x columns of W of a tile, and the
+// CTAs that share its contraction.  The tile names the kernel: e4m3 128 x 256 has the
+// rows on the lanes (grouped_fp8.cuh), bf16 256 x 256 is a CTA pair's.
+struct GroupedPlan {
+  int rows, cols, splits;
+};
+
+// Tile shape by the rows of an average group and the tiles there are (times in us;
+// bf16 unless e4m3 is said):
+//   32 rows x 128 columns where such tiles fit one wave, whatever the rows: a CTA
+//     streams some 75 GB/s, so they have to be many.  n = 1, 4096 x 4096: 9.7
+//     against 11.8 with 512 columns a tile; e4m3 333 x 1000 x 1522: 5.2 against 8.9.
+//     Not where an e4m3 tile would have more than 16 blocks to itself: each costs its
+//     epilogue 0.45 us (1 x 4096 x 14336: 17.3 against 14.9).
+//   16 x 256, two CTAs per SM, up to 16 rows: e4m3 256 x 2048 x 1536 of 128 groups
+//     57 against 59 with 16 x 512 and one CTA.
+//   32 x 256 up to 32 rows: 2400 x 2048 x 1408 of 100 groups 91 against 95 with 16 or
+//     64 rows, or 512 columns; e4m3 32 x 512, whose blocks are half as long to load:
+//     54 against 59 with 256 columns and 60 with 64 rows, but not for a matrix of one
+//     such tile (1989 x 8330 x 218 of 120: 71 against 49 with 64 rows).
+//     Up to 40 rows where columns past the edge weigh little (2600 x 2048 x 1408 of 64:
+//     43 against 46 with 64 rows; 47 rows a group, 3000 x 1024 x 1408 of 64: 28 against 25).
+//   bf16 128 x 256 for 41 to 64 rows, which leave many groups a second tile of 64, where
+//     such tiles fill three quarters of their waves (2600 x 2048 x 1408 of 64: 64 against
+//     70 with 64 rows, 2000 x 2048 x 2048 of 32 48 against 53, 512 x 4096 x 14336 of 8 157
+//     against 169; 3000 x 4096 x 1024 of 48, 192 tiles: 79 against 68).
+//   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
+//     83 with 32; and for more rows where there are few larger tiles (256 x 4096 x 4096:
+//     20 against 24 with 256 rows, e4m3 16 against 19 with 128; 512 x 4096 x 4096, the
+//     other side: 28 against 25, e4m3 20 against 20).
+//   bf16: 256 x 256 on CTA pairs for more.
+//   e4m3: 128 x 256, rows on the lanes, for more (grouped_fp8.cuh): 768 x 4096 x 14336
+//     of 8 103 against 125 with 64 rows, 512 of 8 102 against 100.
+GroupedPlan grouped_plan(bool fp8, int64_t n, int64_t d, int64_t m, int64_t groups, int64_t sms) {
+  // tiles that a call is taken to have: its groups as even as they can be, one tile at
+  // least for each (the bounds are on the device)
+  auto tiles_of = [&](int64_t rows, int64_t cols) {
+    return std::max(ceil_div(n, rows), std::min(groups, n)) * ceil_div(m, cols);
+  };
+  const int64_t rows = ceil_div(n, groups);  // of an average group
+  const int64_t small = tiles_of(32, 128), tiles = tiles_of(128, 256), waves = ceil_div(tiles, sms);
+  const bool few = fp8 ? 5 * tiles < 2 * sms : 5 * tiles_of(256, 256) < sms;
+  GroupedPlan t{};
+  int64_t occ = 1;  // CTAs per SM
+  if (small <= sms && (!fp8 || 2 * small <= sms || d <= 2048)) {
+    t = {32, 128, 1};
+  } else if (rows <= 16) {
+    t = {16, 256, 1};
+    occ = 2;
+  } else if (rows <= (fp8 && m >= 1024 ? 40 : 32) && (!fp8 || m > 256)) {
+    t = {32, fp8 ? 512 : 256, 1};
+  } else if (!fp8 && !few && rows > 40 && rows <= 64 && 4 * tiles >= 3 * waves * sms) {
+    t = {128, 256, 1};
+  } else if (rows <= 64 || few) {
+    t = {64, 256, 1};
+  } else {
+    return {fp8 ? 128 : 256, 256, 1};
+  }
+  // Few tiles: split each one's contraction over a cluster so that about every SM has
+  // a part (n = 1, 4096 x 4096 e4m3: 13.6 us whole, 7.6 us with clusters of 4).
+  // Clusters of 4 reach 132 of 148 SMs and those of 8 only 120, and theirs cost more
+  // to gather (the same call with clusters of 8: 9.0 us), so they are left to calls of
+  // few and long tiles (7 x 11200 x 246 of 3 groups: 11.5 us against 16.2 with 4).
+  // A launch has a cluster for every tile that there may be.
+  const int64_t own = tiles_of(t.rows, t.cols), num_kb = ceil_div(d, fp8 ? 128 : 64);
+  if (2 * own <= sms * occ && num_kb >= 2) t.splits = 2;
+  if (4 * own <= (sms - 16) * occ && num_kb >= 4) t.splits = 4;
+  if (8 * own <= 2 * sms / 3 && num_kb >= 32) t.splits = 8;
+  return t;
 }
 
+
 template <bool FP8, int N, int MT, int CG, int OCC = 1>
-rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
+rmm_status launch_grouped_t(const GroupedCall& c, int splits, cudaStream_t s) {
   using Cfg = GroupedCfg<FP8, N, MT, CG, OCC>;
   CUtensorMap tw, tx;
   if (rmm_status st = make_tmaps_grouped(&tw, &tx, FP8, c.W, c.groups, c.d, c.m, c.ldw, c.w_stride, c.X, c.n, c.ldx,
@@ -1961,20 +2027,7 @@ rmm_status launch_grouped_t(const GroupedCall& c, cudaStream_t s) {
   const int64_t row_tiles = ceil_div(c.n, N) + std::min<int64_t>(c.groups - 1, c.n);
   // (a tile of the last wave may be cut into up to eight)
   if (8 * row_tiles * p.m_tiles > kIntMax) return fail(RMM_ERR_UNSUPPORTED, "too many output tiles");
-  // Few tiles: split each one's contraction over a cluster so that about every SM has
-  // a part (n = 1, 4096 x 4096 e4m3: 13.6 us whole, 7.6 us with clusters of 4).
-  // Clusters of 4 reach 132 of 148 SMs and those of 8 only 120, and theirs cost more
-  // to gather (the same call with clusters of 8: 9.0 us), so they are left to calls of
-  // few and long tiles (7 x 11200 x 246 of 3 groups: 11.5 us against 16.2 with 4).
-  // A launch has a cluster for every tile that there may be.
-  int64_t splits = 1;
-  if (CG == 1) {
-    const int64_t tiles = grouped_tiles(c, N, MT * 128);
-    if (2 * tiles <= num_sms() * OCC && p.num_kb >= 2) splits = 2;
-    if (4 * tiles <= (num_sms() - 16) * OCC && p.num_kb >= 4) splits = 4;
-    if (8 * tiles <= 2 * num_sms() / 3 && p.num_kb >= 32) splits = 8;
-  }
-  p.splits = static_cast<int>(splits);
+  p.splits = splits;
   const int64_t workers = splits > 1 ? row_tiles * p.m_tiles : std::min<int64_t>((N >= 128 ? N / 32 : 1) * row_tiles * p.m_tiles, std::max(1, num_sms() * OCC / CG));
   const int smem = Cfg::smem_bytes(static_cast<int>(c.groups));
   auto kern = grouped_kernel<FP8, N, MT, CG, OCC>;
@@ -2025,47 +2078,19 @@ rmm_status launch_grouped_fp8_rows(const GroupedCall& c, cudaStream_t s) {
   return RMM_OK;
 }
 
-// Tile shape by the rows of an average group and the tiles there are (times in us;
-// bf16 unless e4m3 is said):
-//   32 rows x 128 columns where such tiles fit one wave, whatever the rows: a CTA
-//     streams some 75 GB/s, so they have to be many.  n = 1, 4096 x 4096: 9.7
-//     against 11.8 with 512 columns a tile; e4m3 333 x 1000 x 1522: 5.2 against 8.9.
-//     Not where an e4m3 tile would have more than 16 blocks to itself: each costs its
-//     epilogue 0.45 us (1 x 4096 x 14336: 17.3 against 14.9).
-//   16 x 256, two CTAs per SM, up to 16 rows: e4m3 256 x 2048 x 1536 of 128 groups
-//     57 against 59 with 16 x 512 and one CTA.
-//   32 x 256 up to 32 rows: 2400 x 2048 x 1408 of 100 groups 91 against 95 with 16 or
-//     64 rows, or 512 columns; e4m3 32 x 512, whose blocks are half as long to load:
-//     54 against 59 with 256 columns and 60 with 64 rows, but not for a matrix of one
-//     such tile (1989 x 8330 x 218 of 120: 71 against 49 with 64 rows).
-//     Up to 40 rows where columns past the edge weigh little (2600 x 2048 x 1408 of 64:
-//     43 against 46 with 64 rows; 47 rows a group, 3000 x 1024 x 1408 of 64: 28 against 25).
-//   bf16 128 x 256 for 41 to 64 rows, which leave many groups a second tile of 64, where
-//     such tiles fill three quarters of their waves (2600 x 2048 x 1408 of 64: 64 against
-//     70 with 64 rows, 2000 x 2048 x 2048 of 32 48 against 53, 512 x 4096 x 14336 of 8 157
-//     against 169; 3000 x 4096 x 1024 of 48, 192 tiles: 79 against 68).
-//   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
-//     83 with 32; and for more rows where there are few larger tiles (256 x 4096 x 4096:
-//     20 against 24 with 256 rows, e4m3 16 against 19 with 128; 512 x 4096 x 4096, the
-//     other side: 28 against 25, e4m3 20 against 20).
-//   bf16: 256 x 256 on CTA pairs for more.
-//   e4m3: 128 x 256, rows on the lanes, for more (grouped_fp8.cuh): 768 x 4096 x 14336
-//     of 8 103 against 125 with 64 rows, 512 of 8 102 against 100.
 template <bool FP8>
 rmm_status launch_grouped(const GroupedCall& c, cudaStream_t s) {
-  const int64_t rows = ceil_div(c.n, c.groups);  // of an average group
-  const int64_t small = grouped_tiles(c, 32, 128);
-  if (small <= num_sms() && (!FP8 || 2 * small <= num_sms() || c.d <= 2048)) return launch_grouped_t<FP8, 32, 1, 1>(c, s);
-  if (rows <= 16) return launch_grouped_t<FP8, 16, 2, 1, 2>(c, s);
-  if (rows <= (FP8 && c.m >= 1024 ? 40 : 32) && (!FP8 || c.m > 256)) return launch_grouped_t<FP8, 32, FP8 ? 4 : 2, 1>(c, s);
-  const bool few = FP8 ? 5 * grouped_tiles(c, 128, 256) < 2 * num_sms() : 5 * grouped_tiles(c, 256, 256) < num_sms();
-  const int64_t tiles = grouped_tiles(c, 128, 256), waves = ceil_div(tiles, num_sms());
-  if constexpr (!FP8) {
-    if (!few && rows > 40 && rows <= 64 && 4 * tiles >= 3 * waves * num_sms()) return launch_grouped_t<FP8, 128, 2, 1>(c, s);
+  const GroupedPlan t = grouped_plan(FP8, c.n, c.d, c.m, c.groups, num_sms());
+  if (t.rows == 16) return launch_grouped_t<FP8, 16, 2, 1, 2>(c, t.splits, s);
+  if (t.rows == 32 && t.cols == 128) return launch_grouped_t<FP8, 32, 1, 1>(c, t.splits, s);
+  if (t.rows == 32) return launch_grouped_t<FP8, 32, FP8 ? 4 : 2, 1>(c, t.splits, s);
+  if (t.rows == 64) return launch_grouped_t<FP8, 64, 2, 1>(c, t.splits, s);
+  if constexpr (FP8) {
+    return launch_grouped_fp8_rows(c, s);
+  } else {
+    if (t.rows == 128) return launch_grouped_t<false, 128, 2, 1>(c, t.splits, s);
+    return launch_grouped_t<false, 256, 1, 2>(c, t.splits, s);
   }
-  if (rows <= 64 || few) return launch_grouped_t<FP8, 64, 2, 1>(c, s);
-  if constexpr (FP8) return launch_grouped_fp8_rows(c, s);
-  else return launch_grouped_t<false, 256, 1, 2>(c, s);
 }
 
 constexpr const char* kInPlace = "Y must not be X or W: tiles read them while others write Y";
@@ -2251,6 +2276,19 @@ rmm_status rmm_grouped_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int6
   if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
   return fp8_product(Xq, n, d, ldx, sx, lds, Wq, groups, w_stride, m, ldw, sw, offsets, Y, ldy,
                      static_cast<cudaStream_t>(stream));
+}
+
+rmm_status rmm_debug_grouped_plan(int e4m3, int64_t n, int64_t d, int64_t m, int64_t groups, int32_t sms,
+                                  int32_t* plan_out) {
+  t_last_error.clear();
+  if (plan_out == nullptr) return fail(RMM_ERR_INVALID_ARG, "plan_out is required");
+  if (n < 1 || d < 1 || m < 1 || groups < 1 || sms < 1 || (e4m3 != 0 && e4m3 != 1))
+    return fail(RMM_ERR_INVALID_ARG, "n, d, m, groups and sms must be >= 1, e4m3 0 or 1");
+  const GroupedPlan t = grouped_plan(e4m3 != 0, n, d, m, groups, sms);
+  plan_out[0] = t.rows;
+  plan_out[1] = t.cols;
+  plan_out[2] = t.splits;
+  return RMM_OK;
 }
 
 }  // extern "C"

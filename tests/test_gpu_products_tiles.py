@@ -1,0 +1,33 @@
+"""The grouped and fp8 products by tile: every kernel, every split of a contraction and every number of scale blocks
+that the choice of tiles reaches, against the formula in 64 bits."""
+import pytest
+import torch
+
+from grouped_cases import CASES, Operands, case_id, plan
+
+pytestmark = pytest.mark.gpu
+
+rmm = pytest.importorskip("input_adaptive_reduced_colnorm_b200")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from input_adaptive_reduced_colnorm_b200 import build
+    build.build()
+    yield
+    assert rmm.device_error() == 0
+
+
+@pytest.mark.parametrize("case", CASES, ids=case_id)
+def test_tile(case):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    o = Operands(case)
+    assert plan(o.dtype, o.n, o.d, o.m, o.groups, sms) == case[4]
+    out = o.out()
+    o.call(out)
+    o.check(out, *o.reference())
+    behind = out.as_strided((o.n, out.stride(0)), (out.stride(0), 1))[:, o.m:]
+    assert behind.isnan().all()  # the buffer's columns past m are as they were
+    again = o.out()
+    o.call(again)
+    assert torch.equal(again, out)  # the same result every time

@@ -1,0 +1,39 @@
+"""The choice of tiles of the grouped and fp8 products (host only): each case of the GPU tests takes the tile that it
+is listed for."""
+import pytest
+
+from grouped_cases import BF16, CASES, E4M3, SMS, case_id, plan
+from input_adaptive_reduced_colnorm_b200 import build as rmm_build
+import input_adaptive_reduced_colnorm_b200 as rmm
+
+OK, INVALID = 0, 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    rmm_build.build()
+
+
+@pytest.mark.parametrize("case", CASES, ids=case_id)
+def test_cases_take_their_tiles(case):
+    dtype, sizes, d, m, tile = case
+    outside = 5 if len(sizes) > 1 else 0
+    assert plan(dtype, sum(sizes) + outside, d, m, len(sizes)) == tile
+
+
+def test_every_tile_has_a_case():
+    """Over a grid of sizes nothing is chosen that the cases leave out."""
+    sizes = (1, 7, 16, 17, 33, 64, 65, 200, 513, 1030, 4096, 8192)
+    widths = (1, 130, 300, 1000, 1522, 2048, 2600, 4096, 6000, 9000, 14336, 20000, 40000)
+    seen = {(t, plan(t, n, d, m, g)) for t in (BF16, E4M3) for n in sizes for d in (1, 130, 300, 1000, 2200, 4200, 14336)
+            for m in widths for g in (1, 2, 3, 8, 20, 64, 128)}
+    assert seen == {(c[0], c[4]) for c in CASES}
+
+
+def test_plan_refusals():
+    import ctypes
+    L, out = rmm.lib(), ctypes.cast((ctypes.c_int32 * 3)(), ctypes.c_void_p)
+    good = (1, 8, 256, 512, 2, SMS, out)
+    assert L.rmm_debug_grouped_plan(*good) == OK
+    for i, bad in ((0, 2), (1, 0), (2, 0), (3, 0), (4, 0), (5, 0), (6, None)):
+        assert L.rmm_debug_grouped_plan(*good[:i], bad, *good[i + 1:]) == INVALID
