@@ -418,11 +418,20 @@ rmm_status rmm_debug_gemm_expire_producer(const rmm_bf16* A_pack, int64_t n, int
                                           const rmm_bf16* B_pack, int64_t m, int64_t ldb, rmm_bf16* Y, int64_t ldy,
                                           rmm_stream stream);
 
-/* rmm_debug_grouped_plan: how rmm_grouped_linear (e4m3 = 0) or
+/* rmm_debug_grouped_expire_producer: the same for rmm_grouped_linear (e4m3 = 0, the
+ * scales are ignored) or rmm_grouped_linear_fp8 (1), whatever tile the call takes: the
+ * producers of all CTAs that have more blocks of the contraction than stages (at most 8
+ * blocks of 128 bytes) run out of time.
+ *
+ * rmm_debug_grouped_plan: how rmm_grouped_linear (e4m3 = 0) or
  * rmm_grouped_linear_fp8 (1; rmm_linear_fp8 with groups = 1) tiles a call on a GPU
  * of `sms` SMs: plan_out[0] rows of X and plan_out[1] columns of W of a tile,
  * plan_out[2] CTAs that share one's contraction.  Host only: no device is touched;
  * plan_out is host memory. */
+rmm_status rmm_debug_grouped_expire_producer(int e4m3, const void* X, int64_t n, int64_t d, int64_t ldx, const float* sx,
+                                             int64_t lds, const void* W, int64_t groups, int64_t w_stride, int64_t m,
+                                             int64_t ldw, const float* sw, const int32_t* offsets, rmm_bf16* Y,
+                                             int64_t ldy, rmm_stream stream);
 rmm_status rmm_debug_grouped_plan(int e4m3, int64_t n, int64_t d, int64_t m, int64_t groups, int32_t sms,
                                   int32_t* plan_out);
 

@@ -81,6 +81,8 @@ _SIGNATURES = {
                                     _c_i64, _c_p]),
     "rmm_grouped_linear_fp8": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64,
                                         _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p]),
+    "rmm_debug_grouped_expire_producer": (_c_int, [_c_int, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64,
+                                                   _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p]),
     "rmm_debug_grouped_plan": (_c_int, [_c_int, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32, _c_p]),
     "rmm_status_string": (ctypes.c_char_p, [_c_int]),
     "rmm_last_error": (ctypes.c_char_p, []),

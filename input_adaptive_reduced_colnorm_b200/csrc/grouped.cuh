@@ -51,6 +51,10 @@
 // warps a scheduler do not cover that).  CG = 2: two CTAs of a cluster form one M = 256
 // product (256 columns of W x 256 rows of X), each staging its own 128 columns of W
 // and half of the rows.
+//
+// Every role asks after a wait whether all its lanes had it fulfilled: when one runs
+// out, lanes may see the barrier, the timer and the abort word at different polls, and a
+// warp of which some lanes left would hang in its next shuffle or tensor-memory load.
 #pragma once
 #include <cuda_bf16.h>
 #include "ptx.cuh"
@@ -73,7 +77,13 @@ struct GroupedParams {
   int64_t lds;
   const float* sw;         // [groups][num_kb][sw_cols]
   int sw_cols;
+  // test hook (0 in every product call): 1 makes each producer, once its stages have
+  // been filled, wait on a barrier that nothing arrives on, with a 1 ms limit, so that
+  // its bounded wait runs out and the kernel takes its timeout path
+  int expire_producer_waits;
 };
+
+constexpr uint64_t kGroupedHookWaitNs = 1000ull * 1000ull;
 
 template <bool FP8, int N, int MT, int CG, int OCC>
 struct GroupedCfg {
@@ -95,7 +105,7 @@ struct GroupedCfg {
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static_assert(STAGES >= 3, "at least three stages");
   static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory");
-  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier area");
+  static_assert(8 * (2 * STAGES + 6) + 8 <= 256, "barrier area");
   static int smem_bytes(int groups) {
     return 1024 + STAGES * (A_BYTES + X_BYTES) + SCALE_BYTES + OUT_BYTES + 256 + (2 * groups + 2) * 4;
   }
@@ -291,7 +301,8 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // even CTA
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* never = drain + 1;  // never completes: the test hook's expiring wait
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   int* pre = off + p.groups + 1;
@@ -314,6 +325,7 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
       mbar_init(&tempty[a], EW * CG);
     }
     mbar_init(drain, FP8 ? 2 : 1);
+    mbar_init(never, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -346,6 +358,7 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
     const uint32_t full_even = CG == 2 ? map_shared_rank(smem_u32(&full[0]), 0u) : 0u;
     int stage = 0;
     uint32_t phase = 0, issued = 0;
+    const uint32_t expire_at = p.expire_producer_waits ? STAGES : 0xffffffffu;
     bool ok = true;
     for (int unit = worker; ok && unit < units.count; unit += workers) {
       const GroupedTile t = units.get(unit);
@@ -354,7 +367,10 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
       const int row = t.row0 + static_cast<int>(rank) * (t.w / 2);  // half of a pair's rows
       const int x_boxes = CG == 2 ? 1 : (t.w + C::X_BOX - 1) / C::X_BOX;  // those that hold rows of the tile
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer))) {
+        const bool expire = issued == expire_at;  // (the test hook)
+        if (!__all_sync(0xffffffffu, mbar_wait(expire ? never : &empty[stage], expire ? 0u : phase ^ 1u, abort_flag,
+                                               kDevErrTimeoutProducer, 0, kMbarCta,
+                                               expire ? kGroupedHookWaitNs : kWaitTimeoutNs))) {
           ok = false;
           break;
         }
@@ -549,7 +565,8 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
             if (i * 32 + lane < HC) sc[i * 32 + lane] = nx[i] * nw[i];
           __syncwarp();
           if (kb + 2 < kb_end) load_scales(kb + 2, nx, nw);
-          if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)) return false;
+          if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue)))
+            return false;
           tc_fence_after();
           const uint32_t base = lane_base + acc * C::COLS;
           // two 8-column groups at a time, the next two on their way
@@ -593,7 +610,8 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
           grouped_store(p, out, sum[g], t.row0 + r_of(g * 8), t.row_end, (mblock0 + mt_of(g * 8)) * 128 + quarter * 32, lane);
       } else {
         const uint32_t acc = acc_i & 1u;
-        if (!mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue, 64)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue, 64)))
+          break;
         tc_fence_after();
         const uint32_t base = lane_base + acc * C::COLS;
 #pragma unroll 4

@@ -49,7 +49,7 @@ struct GroupedFp8Cfg {
   static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 40, EPI_REGS = 232;
   static_assert(OTHER_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "three warpgroups share what was launched");
   static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + OUT_BYTES + 256 + (2 * groups + 2) * 4; }
-  static_assert(8 * (2 * STAGES + 9) + 8 <= 256, "barrier area");
+  static_assert(8 * (2 * STAGES + 10) + 8 <= 256, "barrier area");
 };
 
 // sum[0..15] += v[0..15] * s between the question whether a phase of a barrier is
@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 4;  // both [accumulator][half]
   uint64_t* drain = tempty + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* never = drain + 1;  // never completes: the test hook's expiring wait
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   int* pre = off + p.groups + 1;
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
       mbar_init(&tempty[a], 4);  // four epilogue warps
     }
     mbar_init(drain, 2);
+    mbar_init(never, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -175,11 +177,15 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     // (elected lane of a warp that runs the loop together, as below)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
+    const uint32_t expire_at = p.expire_producer_waits ? STAGES : 0xffffffffu;
     bool ok = true;
     for (int unit = worker; ok && unit < units.count; unit += workers) {
       const GroupedTile t = units.get(unit);
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer))) {
+        const bool expire = issued == expire_at;  // (the test hook)
+        if (!__all_sync(0xffffffffu, mbar_wait(expire ? never : &empty[stage], expire ? 0u : phase ^ 1u, abort_flag,
+                                               kDevErrTimeoutProducer, 0, kMbarCta,
+                                               expire ? kGroupedHookWaitNs : kWaitTimeoutNs))) {
           ok = false;
           break;
         }
@@ -304,7 +310,8 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 128; ++i) sum[i] = 0.f;
       uint32_t r[2][16];
-      ok = mbar_wait(&tfull[(acc_i & 1u) * 2 + half], (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
+      ok = __all_sync(0xffffffffu, mbar_wait(&tfull[(acc_i & 1u) * 2 + half], (acc_i >> 1) & 1u, abort_flag,
+                                             kDevErrTimeoutEpilogue));
       if (!ok) break;
       tc_fence_after();
       tmem_ld16(base + (acc_i & 1u) * 256, r[0]);
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
             __syncwarp();
             if (elect_one()) mbar_arrive(&tempty[acc * 2 + half]);
             if (kb + 1 < p.num_kb && __any_sync(0xffffffffu, !ready))
-              ok = mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue);
+              ok = __all_sync(0xffffffffu, mbar_wait(next_full, (acc_i >> 1) & 1u, abort_flag, kDevErrTimeoutEpilogue));
             tc_fence_after();
             tmem_ld16(base + (acc ^ 1u) * 256, r[0]);  // (after the last block: not used)
           }

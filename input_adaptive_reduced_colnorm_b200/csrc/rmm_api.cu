@@ -2127,7 +2127,7 @@ rmm_status check_scales(const float* sx, int64_t lds, int64_t n, const float* sw
 
 rmm_status fp8_product(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
                        const rmm_e4m3* Wq, int64_t groups, int64_t w_stride, int64_t m, int64_t ldw, const float* sw,
-                       const int32_t* offsets, rmm_bf16* Y, int64_t ldy, cudaStream_t s) {
+                       const int32_t* offsets, rmm_bf16* Y, int64_t ldy, cudaStream_t s, int expire = 0) {
   if (rmm_status st = check_product(Xq, n, d, ldx, Wq, groups, w_stride, m, ldw, Y, ldy, 16)) return st;
   if (rmm_status st = check_scales(sx, lds, n, sw)) return st;
   if (n == 0) return RMM_OK;
@@ -2152,7 +2152,41 @@ rmm_status fp8_product(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, co
   c.p.lds = lds;
   c.p.sw = sw;
   c.p.sw_cols = static_cast<int>(ceil_div(m, 128));
+  c.p.expire_producer_waits = expire;
   return launch_grouped<true>(c, s);
+}
+
+rmm_status check_offsets(const int32_t* offsets) {
+  if (offsets == nullptr) return fail(RMM_ERR_INVALID_ARG, "offsets are required");
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
+  return RMM_OK;
+}
+
+rmm_status bf16_product(const rmm_bf16* X, int64_t n, int64_t d, int64_t ldx, const rmm_bf16* W, int64_t groups,
+                        int64_t w_stride, int64_t m, int64_t ldw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy,
+                        cudaStream_t s, int expire = 0) {
+  if (rmm_status st = check_product(X, n, d, ldx, W, groups, w_stride, m, ldw, Y, ldy, 8)) return st;
+  if (rmm_status st = check_offsets(offsets)) return st;
+  if (n == 0) return RMM_OK;
+  if (Y == X || Y == W) return fail(RMM_ERR_INVALID_ARG, kInPlace);
+  GroupedCall c{};
+  c.X = X;
+  c.n = n;
+  c.d = d;
+  c.ldx = ldx;
+  c.W = W;
+  c.groups = groups;
+  c.w_stride = w_stride;
+  c.m = m;
+  c.ldw = ldw;
+  c.p.offsets = offsets;
+  c.p.groups = static_cast<int>(groups);
+  c.p.n = static_cast<int>(n);
+  c.p.m = static_cast<int>(m);
+  c.p.Y = Y;
+  c.p.ldy = ldy;
+  c.p.expire_producer_waits = expire;
+  return launch_grouped<false>(c, s);
 }
 
 }  // namespace
@@ -2244,38 +2278,31 @@ rmm_status rmm_grouped_linear(const rmm_bf16* X, int64_t n, int64_t d, int64_t l
                               int64_t w_stride, int64_t m, int64_t ldw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy,
                               rmm_stream stream) {
   t_last_error.clear();
-  if (rmm_status st = check_product(X, n, d, ldx, W, groups, w_stride, m, ldw, Y, ldy, 8)) return st;
-  if (offsets == nullptr) return fail(RMM_ERR_INVALID_ARG, "offsets are required");
-  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
-  if (n == 0) return RMM_OK;
-  if (Y == X || Y == W) return fail(RMM_ERR_INVALID_ARG, kInPlace);
-  GroupedCall c{};
-  c.X = X;
-  c.n = n;
-  c.d = d;
-  c.ldx = ldx;
-  c.W = W;
-  c.groups = groups;
-  c.w_stride = w_stride;
-  c.m = m;
-  c.ldw = ldw;
-  c.p.offsets = offsets;
-  c.p.groups = static_cast<int>(groups);
-  c.p.n = static_cast<int>(n);
-  c.p.m = static_cast<int>(m);
-  c.p.Y = Y;
-  c.p.ldy = ldy;
-  return launch_grouped<false>(c, static_cast<cudaStream_t>(stream));
+  return bf16_product(X, n, d, ldx, W, groups, w_stride, m, ldw, offsets, Y, ldy, static_cast<cudaStream_t>(stream));
 }
 
 rmm_status rmm_grouped_linear_fp8(const rmm_e4m3* Xq, int64_t n, int64_t d, int64_t ldx, const float* sx, int64_t lds,
                                   const rmm_e4m3* Wq, int64_t groups, int64_t w_stride, int64_t m, int64_t ldw,
                                   const float* sw, const int32_t* offsets, rmm_bf16* Y, int64_t ldy, rmm_stream stream) {
   t_last_error.clear();
-  if (offsets == nullptr) return fail(RMM_ERR_INVALID_ARG, "offsets are required");
-  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fail(RMM_ERR_UNSUPPORTED, "offsets must be 4-byte aligned");
+  if (rmm_status st = check_offsets(offsets)) return st;
   return fp8_product(Xq, n, d, ldx, sx, lds, Wq, groups, w_stride, m, ldw, sw, offsets, Y, ldy,
                      static_cast<cudaStream_t>(stream));
+}
+
+rmm_status rmm_debug_grouped_expire_producer(int e4m3, const void* X, int64_t n, int64_t d, int64_t ldx, const float* sx,
+                                             int64_t lds, const void* W, int64_t groups, int64_t w_stride, int64_t m,
+                                             int64_t ldw, const float* sw, const int32_t* offsets, rmm_bf16* Y,
+                                             int64_t ldy, rmm_stream stream) {
+  t_last_error.clear();
+  if (e4m3 != 0 && e4m3 != 1) return fail(RMM_ERR_INVALID_ARG, "e4m3 must be 0 or 1");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (e4m3 == 0)
+    return bf16_product(static_cast<const rmm_bf16*>(X), n, d, ldx, static_cast<const rmm_bf16*>(W), groups, w_stride, m,
+                        ldw, offsets, Y, ldy, s, 1);
+  if (rmm_status st = check_offsets(offsets)) return st;
+  return fp8_product(static_cast<const rmm_e4m3*>(X), n, d, ldx, sx, lds, static_cast<const rmm_e4m3*>(W), groups,
+                     w_stride, m, ldw, sw, offsets, Y, ldy, s, 1);
 }
 
 rmm_status rmm_debug_grouped_plan(int e4m3, int64_t n, int64_t d, int64_t m, int64_t groups, int32_t sms,

@@ -60,6 +60,35 @@ CASES = [
     (E4M3, [300], 12400, 5120, (128, 256, 1)),
 ]
 
+# the same tiles, every CTA with more blocks of the contraction than a kernel has stages
+LONG = [
+    (BF16, [20], 2100, 18000, (32, 128, 1)),
+    (BF16, [7], 2100, 9000, (32, 128, 2)),
+    (BF16, [20], 4200, 4200, (32, 128, 4)),
+    (BF16, [9, 0, 30, 1], 6100, 300, (32, 128, 8)),
+    (E4M3, [20], 2048, 18000, (32, 128, 1)),
+    (E4M3, [7], 2560, 9000, (32, 128, 2)),
+    (E4M3, [20], 4800, 4200, (32, 128, 4)),
+    (E4M3, [9, 0, 30, 1], 9300, 300, (32, 128, 8)),
+    (BF16, [3, 0, 16, 1, 17, 9], 2100, 8200, (16, 256, 1)),
+    (BF16, [5], 2100, 20000, (16, 256, 2)),
+    (E4M3, [3, 0, 16, 1, 17, 9], 2100, 8200, (16, 256, 1)),
+    (E4M3, [5], 2100, 20000, (16, 256, 2)),
+    (E4M3, [13], 2176, 14336, (16, 256, 4)),
+    (BF16, [30, 1, 33, 32, 0, 16, 40, 31], 2100, 2600, (32, 256, 1)),
+    (E4M3, [40, 1, 33, 32, 0, 36, 40, 31] * 2, 2100, 6000, (32, 512, 1)),
+    (E4M3, [20], 2100, 20000, (32, 512, 2)),
+    (E4M3, [20], 2200, 12000, (32, 512, 4)),
+    (BF16, [128, 60, 0, 1, 33, 31, 100, 64, 17, 16], 2100, 3500, (128, 256, 1)),
+    (BF16, [64, 70, 0, 1, 63, 40, 65, 64, 50, 60], 2100, 4100, (64, 256, 1)),
+    (BF16, [200], 2100, 2900, (64, 256, 2)),
+    (E4M3, [64, 70, 0, 1, 63, 40, 65, 64, 50, 60], 2100, 4100, (64, 256, 1)),
+    (E4M3, [200], 2100, 2900, (64, 256, 2)),
+    (E4M3, [64], 3200, 5000, (64, 256, 4)),
+    (BF16, [150, 20, 300], 2100, 8100, (256, 256, 1)),
+    (E4M3, [150, 20, 300], 2100, 4100, (128, 256, 1)),
+]
+
 
 def case_id(c):
     return f"{'e4m3' if c[0] else 'bf16'}-{'x'.join(map(str, c[4]))}-{sum(c[1])}of{len(c[1])}-{c[2]}x{c[3]}"
@@ -108,6 +137,14 @@ class Operands:
         if self.dtype:
             return rmm.grouped_linear_fp8(self.X, self.sx, self.W, self.sw, self.off, out=out)
         return rmm.grouped_linear(self.X, self.W, self.off, out=out)
+
+    def expire(self, out):
+        """The same call with the producers' waits made to run out."""
+        sx, lds, sw = (self.sx.data_ptr(), self.n, self.sw.data_ptr()) if self.dtype else (None, 0, None)
+        return rmm.lib().rmm_debug_grouped_expire_producer(
+            self.dtype, self.X.data_ptr(), self.n, self.d, self.X.stride(0), sx, lds, self.W.data_ptr(), self.groups,
+            self.W.stride(0), self.m, self.W.stride(1), sw, self.off.data_ptr(), out.data_ptr(), out.stride(0),
+            torch.cuda.current_stream().cuda_stream)
 
     def out(self, fill=3.0):
         y = wider((self.n, self.m), 8, torch.bfloat16)

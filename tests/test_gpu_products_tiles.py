@@ -1,9 +1,10 @@
 """The grouped and fp8 products by tile: every kernel, every split of a contraction and every number of scale blocks
-that the choice of tiles reaches, against the formula in 64 bits."""
+that the choice of tiles reaches, against the formula in 64 bits; and every kernel with its producers' waits made to
+run out."""
 import pytest
 import torch
 
-from grouped_cases import CASES, Operands, case_id, plan
+from grouped_cases import CASES, LONG, Operands, case_id, plan
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,27 @@ def test_tile(case):
     again = o.out()
     o.call(again)
     assert torch.equal(again, out)  # the same result every time
+
+
+TIMEOUT_PRODUCER = 1
+
+
+@pytest.mark.parametrize("case", LONG, ids=case_id)
+def test_expired_wait_returns_and_leaves_the_context_usable(case):
+    """Producers that stop after their first stages: the other roles leave their waits, the kernel returns with the
+    producer's code, writes nothing outside the groups' rows, and the next call is right."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    o = Operands(case)
+    assert plan(o.dtype, o.n, o.d, o.m, o.groups, sms) == case[4]
+    assert rmm.device_error() == 0
+    out = o.out()
+    assert o.expire(out) == 0, rmm.lib().rmm_last_error()
+    torch.cuda.synchronize()
+    assert rmm.device_error() == TIMEOUT_PRODUCER
+    assert rmm.device_error() == 0  # the read cleared it
+    assert (out[: o.before] == 3).all() and (out[o.n - o.behind:] == 3).all()
+    behind = out.as_strided((o.n, out.stride(0)), (out.stride(0), 1))[:, o.m:]
+    assert behind.isnan().all()
+    o.call(out)
+    o.check(out, *o.reference())
+    assert rmm.device_error() == 0

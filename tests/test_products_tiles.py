@@ -2,7 +2,7 @@
 is listed for."""
 import pytest
 
-from grouped_cases import BF16, CASES, E4M3, SMS, case_id, plan
+from grouped_cases import BF16, CASES, E4M3, LONG, SMS, case_id, plan
 from input_adaptive_reduced_colnorm_b200 import build as rmm_build
 import input_adaptive_reduced_colnorm_b200 as rmm
 
@@ -14,7 +14,7 @@ def built():
     rmm_build.build()
 
 
-@pytest.mark.parametrize("case", CASES, ids=case_id)
+@pytest.mark.parametrize("case", CASES + LONG, ids=case_id)
 def test_cases_take_their_tiles(case):
     dtype, sizes, d, m, tile = case
     outside = 5 if len(sizes) > 1 else 0
@@ -27,7 +27,23 @@ def test_every_tile_has_a_case():
     widths = (1, 130, 300, 1000, 1522, 2048, 2600, 4096, 6000, 9000, 14336, 20000, 40000)
     seen = {(t, plan(t, n, d, m, g)) for t in (BF16, E4M3) for n in sizes for d in (1, 130, 300, 1000, 2200, 4200, 14336)
             for m in widths for g in (1, 2, 3, 8, 20, 64, 128)}
-    assert seen == {(c[0], c[4]) for c in CASES}
+    assert seen == {(c[0], c[4]) for c in CASES} == {(c[0], c[4]) for c in LONG}
+
+
+def test_expiring_hook_refusals():
+    """It checks its arguments as the calls do, and enqueues nothing for no rows."""
+    P = 0x10000
+    L = rmm.lib()
+
+    def f(e4m3, n=0, X=P, off=P, sw=P):
+        return L.rmm_debug_grouped_expire_producer(e4m3, X, n, 256, 256, P, 8, P, 2, 256 * 512, 512, 512, sw, off, P * 2,
+                                                   512, None)
+    assert f(0) == OK and f(1) == OK
+    assert f(2) == INVALID
+    assert f(0, off=None) == INVALID and f(1, off=None) == INVALID
+    assert f(0, n=8, X=None) == INVALID and f(1, n=8, X=None) == INVALID
+    assert f(0, n=8, X=2 * P) == INVALID and f(1, n=8, X=2 * P) == INVALID  # in place
+    assert f(1, sw=None) == INVALID and f(0, sw=None) == OK
 
 
 def test_plan_refusals():
