@@ -20,9 +20,9 @@
 // memory in the 16 x 256-bit shape: a thread gets 2 neighbouring rows of X for 4
 // columns of W out of each 8 x 32, so one pair of row scales (times the weight
 // block's, kept by each warp in shared memory) serves 4 packed multiply-adds.
-// (With a lane's whole row per thread, every multiply-add needed scales of its
-// own: 1 MB of shared-memory reads per 256 x 256 block and SM pair, twice the
-// time of the block's tensor work; 380 TFLOP/s at 4096 x 4096 x 14336.)
+// (With a lane's whole row per thread, every multiply-add needed a scale of its own
+// from shared memory, twice the time of the block's tensor work; 380 TFLOP/s at
+// 4096 x 4096 x 14336, on tiles of 256 x 256.)
 //
 // Bound by HBM with few rows (bf16 64 x 4096 x 14336 of 8 groups: 139 us, the copy
 // bandwidth; e4m3 8 x 8192 x 28672: 39 us, 0.92 of it) and by the tensor cores at the
@@ -48,9 +48,9 @@
 // 2 on epilogue: 8, and 16 for the e4m3 tiles of 128 accumulator columns, whose every
 // block goes through them (64 x 4096 x 14336: 16.5 us against 20.1 with 8; 4096 x 2048 x
 // 1408 of 64 groups 46 against 48; each waits for its loads of tensor memory, and two
-// warps a scheduler do not cover that).  CG = 2: two CTAs of a cluster form one M = 256
-// product (256 columns of W x 256 rows of X), each staging its own 128 columns of W
-// and half of the rows.
+// warps a scheduler do not cover that).  CG = 2 (bf16): two CTAs of a cluster form one
+// M = 256 product (256 columns of W x 256 rows of X), each staging its own 128 columns of
+// W and half of the rows.
 //
 // Every role asks after a wait whether all its lanes had it fulfilled: when one runs
 // out, lanes may see the barrier, the timer and the abort word at different polls, and a
@@ -103,6 +103,7 @@ struct GroupedCfg {
   static constexpr int STAGES_FIT =
       (233472 / OCC - 1024 - 1024 - 256 - SCALE_BYTES - OUT_BYTES - (2 * BOUND_GROUPS + 2) * 4) / (A_BYTES + X_BYTES);
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
+  static_assert(!(FP8 && CG == 2), "pairs are bf16's (see grouped_fp8.cuh for the e4m3 tiles of large groups)");
   static_assert(STAGES >= 3, "at least three stages");
   static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory");
   static_assert(8 * (2 * STAGES + 6) + 8 <= 256, "barrier area");
@@ -471,13 +472,9 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
                 const uint64_t am = ad + static_cast<uint64_t>((mt * 16384 + kk * A_STEP) >> 4);
                 const uint64_t xm = xd + static_cast<uint64_t>((kk * 32) >> 4);
                 const uint32_t d = d_tmem + static_cast<uint32_t>(mt * N);
-                if (CG == 2) {
-                  if (FP8) umma_e4m3_pair(d, am, xm, idesc, add);
-                  else umma_bf16_pair(d, am, xm, idesc, add);
-                } else {
-                  if (FP8) umma_e4m3(d, am, xm, idesc, add);
-                  else umma_bf16(d, am, xm, idesc, add);
-                }
+                if (CG == 2) umma_bf16_pair(d, am, xm, idesc, add);
+                else if (FP8) umma_e4m3(d, am, xm, idesc, add);
+                else umma_bf16(d, am, xm, idesc, add);
               }
             }
             if (CG == 2) umma_commit_pair(&empty[stage], 0x3);

@@ -1,5 +1,7 @@
 """The choice of tiles of the grouped and fp8 products (host only): each case of the GPU tests takes the tile that it
 is listed for."""
+import os
+
 import pytest
 
 from grouped_cases import BF16, CASES, E4M3, LONG, SMS, case_id, plan
@@ -53,3 +55,11 @@ def test_plan_refusals():
     assert L.rmm_debug_grouped_plan(*good) == OK
     for i, bad in ((0, 2), (1, 0), (2, 0), (3, 0), (4, 0), (5, 0), (6, None)):
         assert L.rmm_debug_grouped_plan(*good[:i], bad, *good[i + 1:]) == INVALID
+
+
+def test_no_code_for_e4m3_pairs():
+    """e4m3 tiles are single CTAs': their sources hold no pair form of the e4m3 product."""
+    assert plan(E4M3, 8192, 4096, 14336, 8)[:2] == (128, 256)
+    for f in os.listdir(rmm_build.CSRC):
+        with open(os.path.join(rmm_build.CSRC, f)) as h:
+            assert "cta_group::2.kind::f8f6f4" not in h.read(), f
