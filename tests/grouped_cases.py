@@ -60,6 +60,8 @@ CASES = [
     (E4M3, [300], 12400, 5120, (128, 256, 1)),
 ]
 
+GROUPED = [c for c in CASES if len(c[1]) > 1]  # tiles hold rows of other groups
+
 # the same tiles, every CTA with more blocks of the contraction than a kernel has stages
 LONG = [
     (BF16, [20], 2100, 18000, (32, 128, 1)),
@@ -101,10 +103,16 @@ def plan(dtype, n, d, m, groups, sms=SMS):
 
 
 def wider(shape, unit, dtype):
-    """A matrix (or batch) of NaN whose rows are one unit longer than they need, and the view of its columns."""
+    """A matrix in a buffer of NaN whose rows are one unit longer than they need; of a batch, one row longer too."""
     ld = -(-shape[-1] // unit) * unit + unit
-    buf = torch.full((*shape[:-1], ld), float("nan"), device="cuda").to(dtype)
-    return buf[..., : shape[-1]]
+    rows = (*shape[:-2], shape[-2] + 1) if len(shape) > 2 else shape[:-1]
+    buf = torch.full((*rows, ld), float("nan"), device="cuda").to(dtype)
+    return buf[..., : shape[-2], : shape[-1]]
+
+
+def behind_one(t):
+    """t at an address that is a multiple of its element's size only."""
+    return torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)
 
 
 class Operands:
@@ -121,7 +129,7 @@ class Operands:
         self.bounds = [self.before]
         for s in sizes:
             self.bounds.append(self.bounds[-1] + s)
-        self.off = torch.tensor(self.bounds, dtype=torch.int32, device="cuda")
+        self.off = behind_one(torch.tensor(self.bounds, dtype=torch.int32, device="cuda"))
         t, unit = (torch.float8_e4m3fn, 16) if dtype else (torch.bfloat16, 8)
         x = torch.randn((self.n, d), generator=g, device="cuda")
         w = torch.randn((self.groups, d, m), generator=g, device="cuda")
@@ -130,8 +138,10 @@ class Operands:
         self.W.copy_(w)
         if dtype:
             nb, mb = -(-d // 128), -(-m // 128)
-            self.sx = torch.exp2(4 * torch.rand((nb, self.n), generator=g, device="cuda") - 2)
-            self.sw = torch.exp2(4 * torch.rand((self.groups, nb, mb), generator=g, device="cuda") - 2)
+            sx = torch.exp2(4 * torch.rand((nb, self.n + 3), generator=g, device="cuda") - 2)
+            sx[:, self.n:] = float("nan")
+            self.sx = behind_one(sx)[:, : self.n]
+            self.sw = behind_one(torch.exp2(4 * torch.rand((self.groups, nb, mb), generator=g, device="cuda") - 2))
 
     def call(self, out=None):
         if self.dtype:
@@ -140,7 +150,7 @@ class Operands:
 
     def expire(self, out):
         """The same call with the producers' waits made to run out."""
-        sx, lds, sw = (self.sx.data_ptr(), self.n, self.sw.data_ptr()) if self.dtype else (None, 0, None)
+        sx, lds, sw = (self.sx.data_ptr(), self.sx.stride(0), self.sw.data_ptr()) if self.dtype else (None, 0, None)
         return rmm.lib().rmm_debug_grouped_expire_producer(
             self.dtype, self.X.data_ptr(), self.n, self.d, self.X.stride(0), sx, lds, self.W.data_ptr(), self.groups,
             self.W.stride(0), self.m, self.W.stride(1), sw, self.off.data_ptr(), out.data_ptr(), out.stride(0),

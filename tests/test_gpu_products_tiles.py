@@ -4,7 +4,7 @@ run out."""
 import pytest
 import torch
 
-from grouped_cases import CASES, LONG, Operands, case_id, plan
+from grouped_cases import CASES, GROUPED, LONG, Operands, case_id, plan
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,36 @@ def test_expired_wait_returns_and_leaves_the_context_usable(case):
     o.call(out)
     o.check(out, *o.reference())
     assert rmm.device_error() == 0
+
+
+@pytest.mark.parametrize("case", GROUPED, ids=case_id)
+def test_nan_stays_in_its_rows_and_its_group(case):
+    """NaN and infinity in rows of no group, in the weights (and their scales) of a group without rows, in the first
+    row of each second group that has rows, just past the end of another one (in its values, or for e4m3 in the scale
+    of its last block), and in the scale of row 0: only the rows that hold them are NaN."""
+    o = Operands(case)
+    ref, mag = o.reference()
+    nan, t = float("nan"), o.X.dtype
+    sick = torch.zeros(o.n, dtype=torch.bool, device="cuda")
+    with_rows = [e for e in range(o.groups) if o.bounds[e + 1] > o.bounds[e]]
+    for k, e in enumerate(with_rows[1::2]):
+        row = o.bounds[e]
+        sick[row] = True
+        if o.dtype and k % 2:
+            o.sx[-1, row] = nan
+        else:
+            o.X[row, o.d - 1] = torch.tensor(nan).to(t)
+    for e in range(o.groups):
+        if e not in with_rows:
+            o.W[e] = torch.tensor(nan).to(t)
+            if o.dtype:
+                o.sw[e] = nan
+    o.X[: o.before] = torch.tensor(nan).to(t)
+    o.X[o.n - o.behind:] = torch.tensor(nan).to(t)
+    if o.dtype:
+        o.sx[:, : o.before] = nan
+        o.sx[:, o.n - o.behind:] = float("inf")
+    out = o.out()
+    o.call(out)
+    assert out[sick].isnan().all()
+    o.check(out, ref, mag, ~sick)

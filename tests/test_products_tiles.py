@@ -4,7 +4,7 @@ import os
 
 import pytest
 
-from grouped_cases import BF16, CASES, E4M3, LONG, SMS, case_id, plan
+from grouped_cases import BF16, CASES, E4M3, GROUPED, LONG, SMS, case_id, plan
 from input_adaptive_reduced_colnorm_b200 import build as rmm_build
 import input_adaptive_reduced_colnorm_b200 as rmm
 
@@ -30,6 +30,7 @@ def test_every_tile_has_a_case():
     seen = {(t, plan(t, n, d, m, g)) for t in (BF16, E4M3) for n in sizes for d in (1, 130, 300, 1000, 2200, 4200, 14336)
             for m in widths for g in (1, 2, 3, 8, 20, 64, 128)}
     assert seen == {(c[0], c[4]) for c in CASES} == {(c[0], c[4]) for c in LONG}
+    assert {(c[0], c[4][:2]) for c in CASES} == {(c[0], c[4][:2]) for c in GROUPED}
 
 
 def test_expiring_hook_refusals():
