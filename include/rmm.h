@@ -419,9 +419,10 @@ rmm_status rmm_debug_gemm_expire_producer(const rmm_bf16* A_pack, int64_t n, int
                                           rmm_stream stream);
 
 /* rmm_debug_grouped_expire_producer: the same for rmm_grouped_linear (e4m3 = 0, the
- * scales are ignored) or rmm_grouped_linear_fp8 (1), whatever tile the call takes: the
- * producers of all CTAs that have more blocks of the contraction than stages (at most 8
- * blocks of 128 bytes) run out of time.
+ * scales are ignored) or rmm_grouped_linear_fp8 (1), whatever tile the call takes.  The
+ * barriers of empty stages expect an arrival that does not come, and the producers of
+ * all CTAs with more blocks of 128 bytes of the contraction than stages (at most 8) run
+ * out of time.
  *
  * rmm_debug_grouped_plan: how rmm_grouped_linear (e4m3 = 0) or
  * rmm_grouped_linear_fp8 (1; rmm_linear_fp8 with groups = 1) tiles a call on a GPU

@@ -77,9 +77,9 @@ struct GroupedParams {
   int64_t lds;
   const float* sw;         // [groups][num_kb][sw_cols]
   int sw_cols;
-  // test hook (0 in every product call): 1 makes each producer, once its stages have
-  // been filled, wait on a barrier that nothing arrives on, with a 1 ms limit, so that
-  // its bounded wait runs out and the kernel takes its timeout path
+  // test hook (0 in every product call): 1 makes the barriers of empty stages expect one
+  // arrival more than they get and limits the producers' waits to 1 ms, so that the wait
+  // for a stage's second use runs out and the kernel takes its timeout path
   int expire_producer_waits;
 };
 
@@ -106,7 +106,7 @@ struct GroupedCfg {
   static_assert(!(FP8 && CG == 2), "pairs are bf16's (see grouped_fp8.cuh for the e4m3 tiles of large groups)");
   static_assert(STAGES >= 3, "at least three stages");
   static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tensor memory");
-  static_assert(8 * (2 * STAGES + 6) + 8 <= 256, "barrier area");
+  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barrier area");
   static int smem_bytes(int groups) {
     return 1024 + STAGES * (A_BYTES + X_BYTES) + SCALE_BYTES + OUT_BYTES + 256 + (2 * groups + 2) * 4;
   }
@@ -302,8 +302,7 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // even CTA
   uint64_t* drain = tempty + 2;
-  uint64_t* never = drain + 1;  // never completes: the test hook's expiring wait
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   int* pre = off + p.groups + 1;
@@ -319,14 +318,13 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], p.expire_producer_waits ? 2 : 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], EW * CG);
     }
     mbar_init(drain, FP8 ? 2 : 1);
-    mbar_init(never, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
     const uint32_t full_even = CG == 2 ? map_shared_rank(smem_u32(&full[0]), 0u) : 0u;
     int stage = 0;
     uint32_t phase = 0, issued = 0;
-    const uint32_t expire_at = p.expire_producer_waits ? STAGES : 0xffffffffu;
+    const uint64_t limit_ns = p.expire_producer_waits ? kGroupedHookWaitNs : kWaitTimeoutNs;
     bool ok = true;
     for (int unit = worker; ok && unit < units.count; unit += workers) {
       const GroupedTile t = units.get(unit);
@@ -368,10 +366,8 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
       const int row = t.row0 + static_cast<int>(rank) * (t.w / 2);  // half of a pair's rows
       const int x_boxes = CG == 2 ? 1 : (t.w + C::X_BOX - 1) / C::X_BOX;  // those that hold rows of the tile
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        const bool expire = issued == expire_at;  // (the test hook)
-        if (!__all_sync(0xffffffffu, mbar_wait(expire ? never : &empty[stage], expire ? 0u : phase ^ 1u, abort_flag,
-                                               kDevErrTimeoutProducer, 0, kMbarCta,
-                                               expire ? kGroupedHookWaitNs : kWaitTimeoutNs))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer, 0, kMbarCta,
+                                               limit_ns))) {
           ok = false;
           break;
         }

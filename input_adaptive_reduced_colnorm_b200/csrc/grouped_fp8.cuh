@@ -49,7 +49,7 @@ struct GroupedFp8Cfg {
   static constexpr int LAUNCH_REGS = 168, OTHER_REGS = 40, EPI_REGS = 232;
   static_assert(OTHER_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "three warpgroups share what was launched");
   static int smem_bytes(int groups) { return 1024 + STAGES * (X_BYTES + W_BYTES) + OUT_BYTES + 256 + (2 * groups + 2) * 4; }
-  static_assert(8 * (2 * STAGES + 10) + 8 <= 256, "barrier area");
+  static_assert(8 * (2 * STAGES + 9) + 8 <= 256, "barrier area");
 };
 
 // sum[0..15] += v[0..15] * s between the question whether a phase of a barrier is
@@ -134,8 +134,7 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 4;  // both [accumulator][half]
   uint64_t* drain = tempty + 4;
-  uint64_t* never = drain + 1;  // never completes: the test hook's expiring wait
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
   int* pre = off + p.groups + 1;
@@ -145,14 +144,13 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);  // both issuers
+      mbar_init(&empty[s], p.expire_producer_waits ? 3 : 2);  // both issuers
     }
     for (int a = 0; a < 4; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 4);  // four epilogue warps
     }
     mbar_init(drain, 2);
-    mbar_init(never, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&tmW);
@@ -177,15 +175,13 @@ __global__ void __launch_bounds__(GroupedFp8Cfg::THREADS, 1)
     // (elected lane of a warp that runs the loop together, as below)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
-    const uint32_t expire_at = p.expire_producer_waits ? STAGES : 0xffffffffu;
+    const uint64_t limit_ns = p.expire_producer_waits ? kGroupedHookWaitNs : kWaitTimeoutNs;
     bool ok = true;
     for (int unit = worker; ok && unit < units.count; unit += workers) {
       const GroupedTile t = units.get(unit);
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        const bool expire = issued == expire_at;  // (the test hook)
-        if (!__all_sync(0xffffffffu, mbar_wait(expire ? never : &empty[stage], expire ? 0u : phase ^ 1u, abort_flag,
-                                               kDevErrTimeoutProducer, 0, kMbarCta,
-                                               expire ? kGroupedHookWaitNs : kWaitTimeoutNs))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, kDevErrTimeoutProducer, 0, kMbarCta,
+                                               limit_ns))) {
           ok = false;
           break;
         }
