@@ -25,14 +25,14 @@
 // 4096 x 4096 x 14336, on tiles of 256 x 256.)
 //
 // Bound by HBM with few rows (bf16 64 x 4096 x 14336 of 8 groups: 139 us, the copy
-// bandwidth; e4m3 8 x 8192 x 28672: 39 us, 0.92 of it) and by the tensor cores at the
-// power cap with many (8192 x 4096 x 14336 of 8: 685-890 us, 530 cycles a stage of
+// bandwidth; e4m3 8 x 8192 x 28672: 40-41 us, 0.88 of it) and by the tensor cores at the
+// power cap with many (8192 x 4096 x 14336 of 8: 690-890 us, 530 cycles a stage of
 // 512 at 1.3-1.45 GHz).
 //
 // Tiles are cut to the rows that are there: the N of a tile's instructions is
 // its row count rounded up to 16 (32 for a pair), and one CTA copies only the runs of
 // 32 rows that hold some (a pair copies all: with four copies of 32 rows in place of one
-// 2048 x 4096 x 14336 of 8 took 300 us against 230).  When the tiles do not fill a whole
+// 2048 x 4096 x 14336 of 8 took 1.3 times as long).  When the tiles do not fill a whole
 // number of waves, those of the last wave are cut into narrower ones.
 //
 // Few tiles (decoding): the contraction of a tile is split over the 2 to 8 CTAs of
@@ -46,8 +46,8 @@
 //
 // Roles: warp 0 TMA producer, warp 1 (and for e4m3 the last warp) MMA issuer, warps from
 // 2 on epilogue: 8, and 16 for the e4m3 tiles of 128 accumulator columns, whose every
-// block goes through them (64 x 4096 x 14336: 16.5 us against 20.1 with 8; 4096 x 2048 x
-// 1408 of 64 groups 46 against 48; each waits for its loads of tensor memory, and two
+// block goes through them (64 x 4096 x 14336: 17.4 us, 0.82 of the time with 8; 4096 x
+// 2048 x 1408 of 64 groups 46 against 48; each waits for its loads of tensor memory, and two
 // warps a scheduler do not cover that).  CG = 2 (bf16): two CTAs of a cluster form one
 // M = 256 product (256 columns of W x 256 rows of X), each staging its own 128 columns of
 // W and half of the rows.
@@ -352,8 +352,9 @@ __global__ void __launch_bounds__(GroupedCfg<FP8, N, MT, CG, OCC>::THREADS, OCC)
     // ------------------------------------------------------------ producer (both CTAs)
     // (the warp runs the loop together and elects the lane that issues, as the MMA
     // issuers do: the copies' operands then stay in uniform registers; bf16 1 x 4096 x
-    // 14336 30 us against 35 with one lane in the loop, 1024 x 4096 x 14336 of 8 166 against 172;
-    // 8192 x 4096 x 14336 of 8, at the power cap for seconds, 885 against 860)
+    // 14336 21.8 us against 22.4 with one lane in the loop, 1024 x 4096 x 14336 of 8 167
+    // against 174, 1000 x 6000 x 500 of 20 53 against 58; 8192 x 4096 x 14336 of 8, at the
+    // power cap for seconds, 795 and 794)
     const uint32_t full_even = CG == 2 ? map_shared_rank(smem_u32(&full[0]), 0u) : 0u;
     int stage = 0;
     uint32_t phase = 0, issued = 0;

@@ -10,21 +10,25 @@
 // 256 of the 512 cycles; the 16 x 256-bit shape that the swapped form needs reads half
 // as fast, 546 cycles).  What it costs is a group's last tile, 128 rows however few
 // are left.  One CTA, not a pair: a pair stages a third less (32 KB a block and CTA
-// against 48), but that is not what bounds it, and its 256-row tiles leave more of a
-// group's last one empty (1024 x 4096 x 14336 of 8 groups: 123 us against 152;
-// 8192 x 4096 x 14336 of 8: 566 against 600; 8192 x 8192 x 8192: 635 against 625).
+// against 48), but its accumulators' round trip is longer, and its 256-row tiles leave
+// more of a group's last one empty (measured when the choice was made: 1024 x 4096 x
+// 14336 of 8 groups 123 us against 152; 8192 x 4096 x 14336 of 8 566 against 600;
+// 8192 x 8192 x 8192 635 against 625).
 //
 // A block's product is issued as two of half the columns with barriers of their
 // own, so that the two epilogue warps of a scheduler work out of step (one loads
 // and waits while the other multiplies); each takes the next block's first columns
 // out of tensor memory before it adds the last ones of this block.
 //
-// 4096 x 4096 x 14336: 244-288 us, 1670-1970 TFLOP/s at 1.5-1.6 GHz (the power cap).
-// ~880 cycles a block, tile changes included, where the product takes 512.  No one
-// thing bounds it: with a quarter of the products 850 are left, without the additions
-// 790, without both 730 -- staging (48 KB a block, 66 bytes a cycle; copies alone reach
-// 77) and the accumulators' round trip (product, commit, epilogue, hand-back) on the two
-// accumulators of 256 columns that tensor memory holds; ~2500 cycles a tile.
+// 4096 x 4096 x 14336: 234-284 us, 1690-2060 TFLOP/s at 1.36-1.6 GHz (the power cap);
+// 840-910 cycles a block, tile changes included, where the product takes 512.  The
+// product cannot bound this tile: staging alone (48 KB a block; copies alone reach 77
+// bytes a cycle) takes some 640.  Nor does one other thing: of 880 cycles a quarter of
+// the products left 850, no additions 790, neither 730 -- staging and the accumulators'
+// round trip (product, commit, epilogue, hand-back) on the two accumulators of 256
+// columns that tensor memory holds; ~2500 cycles a tile.  The power cap takes the rest:
+// 8192 x 14336 x 4096 of 8 runs at 866 cycles a block and 1.57 GHz in a burst (503 us),
+// at 848 and 1.31 GHz for seconds (576 us).
 //
 // Roles (384 threads): warp 0 TMA producer, warps 1 and 2 MMA issuers, one for each
 // product, warps 4-11 epilogue: warp w reads lanes 32 (w % 4) .. + 31 of one of the two

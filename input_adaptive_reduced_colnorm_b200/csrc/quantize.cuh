@@ -4,11 +4,12 @@
 // Activations: blocks of 1 row x 128 columns (quantize_rows_kernel); weights:
 // blocks of 128 x 128 (quantize_blocks_kernel).
 //
-// Bound by memory (2 bytes read, 1 written per element): 8192 x 14336 takes 55 us,
-// 0.98 of the copy bandwidth, eight 4096 x 14336 weights 213 us, 0.99.  It takes about
-// 10 instructions per element to stay there (packed arithmetic, 8 lanes a block, 32-bit
-// columns, no edge checks where d is a multiple of 16): with 14 the same call took
-// 63 us, with IEEE divisions and 16 lanes a block 94 us, bound by issue slots.  Each
+// Bound by memory (2 bytes read, 1 written per element): 8192 x 14336 takes 55-64 us,
+// 0.84-0.98 of the copy bandwidth, eight 4096 x 14336 weights 208-237 us, 0.91-1.0.  It
+// takes about 10 instructions per element to stay there (packed arithmetic, 8 lanes a
+// block, 32-bit columns, no edge checks where d is a multiple of 16): with 14 the same
+// call took 63 us where it took 55 with 10, with IEEE divisions and 16 lanes a block 94,
+// bound by issue slots.  Each
 // element is read once and stays in registers between the maximum and the division.
 //
 // The division, on packed pairs: q0 = x r, q = q0 + (x - q0 s) r with r ~ 1 / s
@@ -23,7 +24,8 @@
 // The scale itself is a q0-step on 1 / 448: a / 7 is never nearer to an fp32
 // midpoint than 1 / 14 of the last place.  The residuals need their products above
 // the subnormal range: blocks whose maximum is below 2^-90, infinite or NaN take
-// the division itself.
+// the division itself.  (All 5.3e8 pairs of a finite block maximum and a value up to it
+// were compared with the divisions once: the same codes and scales.)
 #pragma once
 #include <cuda_bf16.h>
 #include "ptx.cuh"

@@ -1952,9 +1952,12 @@ struct GroupedPlan {
 // bf16 unless e4m3 is said):
 //   32 rows x 128 columns where such tiles fit one wave, whatever the rows: a CTA
 //     streams some 75 GB/s, so they have to be many.  n = 1, 4096 x 4096: 9.7
-//     against 11.8 with 512 columns a tile; e4m3 333 x 1000 x 1522: 5.2 against 8.9.
+//     against 11.8 with 512 columns a tile; e4m3 333 x 1000 x 1522: 5.2 against 8.9,
+//     bf16 300 x 3000 x 520 11 against 13 with 64 x 256 and splits of 4.
 //     Not where an e4m3 tile would have more than 16 blocks to itself: each costs its
-//     epilogue 0.45 us (1 x 4096 x 14336: 17.3 against 14.9).
+//     epilogue 0.45 us (1 x 4096 x 14336: 17.3 against 14.9).  In bf16 the rule loses where
+//     groups of several such tiles have a long contraction: 1000 x 6000 x 500 of 20 takes
+//     52-89, with 64 x 256 and splits of 2 31.
 //   16 x 256, two CTAs per SM, up to 16 rows: e4m3 256 x 2048 x 1536 of 128 groups
 //     57 against 59 with 16 x 512 and one CTA.
 //   32 x 256 up to 32 rows: 2400 x 2048 x 1408 of 100 groups 91 against 95 with 16 or
@@ -1968,9 +1971,10 @@ struct GroupedPlan {
 //     70 with 64 rows, 2000 x 2048 x 2048 of 32 48 against 53, 512 x 4096 x 14336 of 8 157
 //     against 169; 3000 x 4096 x 1024 of 48, 192 tiles: 79 against 68).
 //   64 x 256 up to 64 rows: 4096 x 2048 x 1408 of 64 65 against 72 with 256 rows and
-//     83 with 32; and for more rows where there are few larger tiles (256 x 4096 x 4096:
-//     20 against 24 with 256 rows, e4m3 16 against 19 with 128; 512 x 4096 x 4096, the
-//     other side: 28 against 25, e4m3 20 against 20).
+//     83 with 32; and for more rows where there are few larger tiles (e4m3 256 x 4096 x
+//     4096: 15 against 18 with 128; 512 x 4096 x 4096, the other side: 20 against 18; bf16
+//     256 x 4096 x 4096: 20 against 24 with 256 rows when the rule was made, against 18 since
+//     the pairs' copies have an elected lane; 512 x 4096 x 4096: 28 against 20).
 //   bf16: 256 x 256 on CTA pairs for more.
 //   e4m3: 128 x 256, rows on the lanes, for more (grouped_fp8.cuh): 768 x 4096 x 14336
 //     of 8 103 against 125 with 64 rows, 512 of 8 102 against 100.
