@@ -431,8 +431,8 @@ rmm_status rmm_debug_gemm_expire_producer(const rmm_bf16* A_pack, int64_t n, int
  * rmm_debug_grouped_plan: how rmm_grouped_linear (e4m3 = 0) or
  * rmm_grouped_linear_fp8 (1; rmm_linear_fp8 with groups = 1) tiles a call on a GPU
  * of `sms` SMs: plan_out[0] rows of X and plan_out[1] columns of W of a tile,
- * plan_out[2] CTAs that share one's contraction.  Host only: no device is touched;
- * plan_out is host memory. */
+ * plan_out[2] CTAs that share one's contraction.  Sizes as those calls take them.
+ * Host only: no device is touched; plan_out is host memory. */
 rmm_status rmm_debug_grouped_expire_producer(int e4m3, const void* X, int64_t n, int64_t d, int64_t ldx, const float* sx,
                                              int64_t lds, const void* W, int64_t groups, int64_t w_stride, int64_t m,
                                              int64_t ldw, const float* sw, const int32_t* offsets, rmm_bf16* Y,

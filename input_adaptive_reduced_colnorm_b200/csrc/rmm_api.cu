@@ -2016,7 +2016,6 @@ GroupedPlan grouped_plan(bool fp8, int64_t n, int64_t d, int64_t m, int64_t grou
   return t;
 }
 
-
 template <bool FP8, int N, int MT, int CG, int OCC = 1>
 rmm_status launch_grouped_t(const GroupedCall& c, int splits, cudaStream_t s) {
   using Cfg = GroupedCfg<FP8, N, MT, CG, OCC>;
@@ -2315,6 +2314,8 @@ rmm_status rmm_debug_grouped_plan(int e4m3, int64_t n, int64_t d, int64_t m, int
   if (plan_out == nullptr) return fail(RMM_ERR_INVALID_ARG, "plan_out is required");
   if (n < 1 || d < 1 || m < 1 || groups < 1 || sms < 1 || (e4m3 != 0 && e4m3 != 1))
     return fail(RMM_ERR_INVALID_ARG, "n, d, m, groups and sms must be >= 1, e4m3 0 or 1");
+  if (n > kIntMax - 256 || m > kIntMax - 512 || d > (1LL << 24) || groups > kGroupedMaxGroups || sms > (1 << 20))
+    return fail(RMM_ERR_UNSUPPORTED, "dimension too large");
   const GroupedPlan t = grouped_plan(e4m3 != 0, n, d, m, groups, sms);
   plan_out[0] = t.rows;
   plan_out[1] = t.cols;

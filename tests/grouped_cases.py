@@ -4,7 +4,6 @@ that choice and the GPU tests of the kernels, and their operands with 64-bit ref
 A tile is (rows of X, columns of W, CTAs that share its contraction).  On 148 SMs.
 """
 import ctypes
-import os
 import zlib
 
 import torch
@@ -117,7 +116,7 @@ def behind_one(t):
 
 class Operands:
     """Random operands of a case: Gaussian bf16 values, or any e4m3 codes with scales that differ from block to block
-    (not from a quantiser: any scales are allowed), two rows before the first group and three behind the last; and
+    (not from a quantiser: any scales are allowed), all in buffers wider than they need; two rows before the first group and three behind the last; and
     what the formula gives for them in 64 bits."""
 
     def __init__(self, case):

@@ -8,7 +8,7 @@ from grouped_cases import BF16, CASES, E4M3, GROUPED, LONG, SMS, case_id, plan
 from input_adaptive_reduced_colnorm_b200 import build as rmm_build
 import input_adaptive_reduced_colnorm_b200 as rmm
 
-OK, INVALID = 0, 1
+OK, INVALID, UNSUPPORTED = range(3)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -56,6 +56,9 @@ def test_plan_refusals():
     assert L.rmm_debug_grouped_plan(*good) == OK
     for i, bad in ((0, 2), (1, 0), (2, 0), (3, 0), (4, 0), (5, 0), (6, None)):
         assert L.rmm_debug_grouped_plan(*good[:i], bad, *good[i + 1:]) == INVALID
+    for i, most in ((1, (1 << 31) - 257), (2, 1 << 24), (3, (1 << 31) - 513), (4, 1024), (5, 1 << 20)):
+        assert L.rmm_debug_grouped_plan(*good[:i], most, *good[i + 1:]) == OK
+        assert L.rmm_debug_grouped_plan(*good[:i], most + 1, *good[i + 1:]) == UNSUPPORTED
 
 
 def test_no_code_for_e4m3_pairs():
